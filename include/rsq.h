@@ -444,6 +444,176 @@ rsq_status rsq_pipe_step(rsq_pipe* pipe, const rsq_state* state_in, const rsq_st
 rsq_status rsq_pipe_sync(rsq_pipe* pipe);
 rsq_status rsq_pipe_streams(const rsq_pipe* pipe, void** copy_in, void** compute, void** copy_out);
 
+/* ---------------------------------------------------------------------------
+ * Scan over whole sequences: prompt processing and training of the layers
+ * whose decode step is above (no counterpart in the method's pages).
+ *
+ * The full-precision recurrence of RSQ_MAMBA2 (RetNet and linear attention
+ * through it, as in the decode step) over sequences of any length, and its
+ * gradient.  Per head, from the sequence's state_in (zero when NULL):
+ *     a_t = decay_t  (or exp(dt_t A) when decay is NULL)
+ *     S_t = a_t S_{t-1} + dt_t B_t x_t^T
+ *     out_t = S_t^T C_t + D x_t
+ * The states are full precision, float [sequences][heads][dk][dv], the layout
+ * of rsq_quantize and rsq_dequantize: a prompt's state_out quantizes into the
+ * decode state, and a stored state dequantizes into state_in.
+ *
+ * rsq_scan_config
+ *   family     RSQ_MAMBA2 (the other families: RSQ_E_UNSUPPORTED)
+ *   in_dtype   type of x, Bm, Cm, out and of their gradients: RSQ_BF16
+ *              (RSQ_F32: RSQ_E_UNSUPPORTED)
+ *   sequences  1 <= sequences <= 65536
+ *   tokens     rows of the token arrays, 0 <= tokens < 2^31 - 2^17
+ *   heads, dk, dv, ngroups: as rsq_config
+ *   ragged     0: every sequence has tokens / sequences tokens (must divide), one
+ *              after the other.  1: sequence i has the rows cu_seqlens[i] ..
+ *              cu_seqlens[i+1] - 1; cu_seqlens is a device int32 array
+ *              [sequences + 1], not decreasing, within [0, tokens] (a bound
+ *              outside is clamped into the array and to the bound before it;
+ *              nothing outside is read or written).  A sequence may be empty:
+ *              its state_out is its state_in.  Rows of no sequence are neither
+ *              read nor written.
+ *
+ * rsq_scan_inputs (device)
+ *   x   [tokens][heads][dv], Bm, Cm [tokens][ngroups][dk] in in_dtype; consecutive
+ *       tokens lie x_stride, b_stride, c_stride elements apart (0: packed; else at
+ *       least the row and a multiple of 8), so that they may be slices of one
+ *       projection's output.
+ *   dt  float [tokens][heads] or NULL (1).  A, D  float [heads]; D NULL: 0.
+ *   decay float [tokens][heads], values >= 0 (0 restarts the state), or NULL:
+ *       exp(dt A), which needs dt and A.
+ *   These arrays, their gradients and cu_seqlens need only 4-byte alignment, so
+ *   that a call may take a piece of a longer array.
+ *
+ * Arithmetic.  Sums, states, decays (products of decays as exponents of sums kept
+ * to twice binary32) and the gradients of gates and states are binary32.  The
+ * operands of the matrix products are bf16: exact where they are inputs; states
+ * and scores that only reach a bf16 output (out, dx, dBm, dCm) are rounded to
+ * bf16 once; those that reach a binary32 output enter as three bf16 terms (24
+ * bits).  Results do not change from run to run (no atomics).  A non-finite x,
+ * Bm, Cm or dt may reach the outputs of up to 127 tokens before it of its own
+ * sequence, besides those after it; other sequences never.
+ *
+ * rsq_scan_workspace: bytes of caller-owned scratch of rsq_scan (backward = 0) or
+ *   rsq_scan_backward (backward = 1), 0 when none is needed.  It holds nothing
+ *   between calls; calls that may overlap need one each (captured graphs that
+ *   run at the same time too).
+ * rsq_scan: out [tokens][heads][dv]; state_in, state_out may be NULL, or the same
+ *   buffer.
+ * rsq_scan_backward: given dout [tokens][heads][dv] (packed) and dstate_out (the
+ *   gradient of state_out, NULL: 0), with the forward call's inputs and state_in.
+ *   Writes what is not NULL of rsq_scan_grads: dx, dBm, dCm (packed, in_dtype; dBm
+ *   and dCm summed over a group's heads), ddt (with decay NULL it includes the way
+ *   through exp(dt A)), dlog_decay (the gradient of log a_t, that is a_t times that
+ *   of a_t; 0 where a_t is 0), dA (needs decay NULL), dD: float; dstate_in: float.
+ *   dA and dD are sums over every sequence.  dstate_in may be dstate_out.
+ * Both: asynchronous, capturable; errors RSQ_E_INVAL, RSQ_E_UNSUPPORTED, RSQ_E_CUDA.
+ * Kernel attributes are set by the first call of a shape on a device: make it
+ * before a stream capture begins. */
+typedef struct {
+    int family;
+    int in_dtype;
+    int sequences;
+    int heads;
+    int dk;
+    int dv;
+    int ngroups;
+    int ragged;
+    int64_t tokens;
+} rsq_scan_config;
+
+typedef struct {
+    const void* x;
+    const void* Bm;
+    const void* Cm;
+    const float* dt;
+    const float* A;
+    const float* D;
+    const float* decay;
+    int64_t x_stride;
+    int64_t b_stride;
+    int64_t c_stride;
+} rsq_scan_inputs;
+
+typedef struct {
+    void* dx;
+    void* dBm;
+    void* dCm;
+    float* ddt;
+    float* dlog_decay;
+    float* dA;
+    float* dD;
+    float* dstate_in;
+} rsq_scan_grads;
+
+rsq_status rsq_scan_workspace(const rsq_scan_config* cfg, int backward, size_t* bytes);
+rsq_status rsq_scan(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs, const int32_t* cu_seqlens,
+                    const float* state_in, float* state_out, void* out, void* workspace,
+                    size_t workspace_bytes, void* stream);
+rsq_status rsq_scan_backward(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs,
+                             const int32_t* cu_seqlens, const float* state_in, const void* dout,
+                             const float* dstate_out, const rsq_scan_grads* grads, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Norms around the mixer (no counterpart in the method's pages).
+ *
+ * rsq_gated_norm: the norm of the decode step's or the scan's output, with its
+ *   gate z.  Over every group of `group` columns of a row:
+ *     RSQ_NORM_GATE (Gated DeltaNet, per head): y = n(x) w silu(z)
+ *     RSQ_GATE_NORM (Mamba-2):                  y = n(x silu(z)) w
+ *   with n(u) = u / sqrt(mean(u^2) + eps), silu(z) = z / (1 + e^-z).  z NULL: no
+ *   gate.  w: float [width].
+ * rsq_residual_norm: the residual add with a scale per column, and the norm
+ *   before the next block (one group per row):
+ *     h = residual + scale x (rounded to h's type);  y = n(h) w
+ *   scale: float [width] or NULL (1).  residual NULL: 0.  h may be residual.
+ * rsq_norm_config
+ *   rows >= 0, width 1..16384, group divides width (0: width).
+ *   x_dtype: of x and dx (RSQ_F32: the decode step's output; RSQ_BF16).
+ *   side_dtype: of z, dz, residual, h, dh, dresidual.  y_dtype: of y and dy.
+ *   x_stride, side_stride: elements between rows of x and of z / residual (0:
+ *   width); every other array is packed.
+ *   eps > 0.  order: RSQ_NORM_GATE or RSQ_GATE_NORM (residual norm: ignored).
+ * Backward passes take what the forward pass read (residual norm: the h it
+ * wrote, packed), and write what is not NULL:
+ *   gated: dx, dz, dw float [width] (dz must be NULL without z);
+ *   residual: dresidual = dh + gradient through y (dh NULL: 0; dresidual may be
+ *   dh), dx = scale dresidual, dscale = sum of dresidual x (x may be NULL when
+ *   dscale is), dw.
+ * dw and dscale are sums over rows in binary32 in a fixed order.  Statistics and
+ * everything between are binary32; each output is rounded once.
+ * rsq_norm_workspace: bytes of caller-owned scratch of the backward calls; calls
+ *   that may overlap need one each.
+ * Asynchronous, capturable; errors RSQ_E_INVAL, RSQ_E_UNSUPPORTED, RSQ_E_CUDA. */
+typedef enum { RSQ_NORM_GATE = 0, RSQ_GATE_NORM = 1 } rsq_norm_order;
+
+typedef struct {
+    int64_t rows;
+    int width;
+    int group;
+    int order;
+    int x_dtype;
+    int side_dtype;
+    int y_dtype;
+    float eps;
+    int64_t x_stride;
+    int64_t side_stride;
+} rsq_norm_config;
+
+rsq_status rsq_norm_workspace(const rsq_norm_config* cfg, size_t* bytes);
+rsq_status rsq_gated_norm(const rsq_norm_config* cfg, const void* x, const void* z, const float* w, void* y,
+                          void* stream);
+rsq_status rsq_gated_norm_backward(const rsq_norm_config* cfg, const void* x, const void* z, const float* w,
+                                   const void* dy, void* dx, void* dz, float* dw, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+rsq_status rsq_residual_norm(const rsq_norm_config* cfg, const void* x, const void* residual,
+                             const float* scale, const float* w, void* h, void* y, void* stream);
+rsq_status rsq_residual_norm_backward(const rsq_norm_config* cfg, const void* x, const void* h,
+                                      const float* scale, const float* w, const void* dy, const void* dh,
+                                      void* dx, void* dresidual, float* dscale, float* dw, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
 const char* rsq_status_string(rsq_status s);
 const char* rsq_last_error(void);
 const char* rsq_version(void);

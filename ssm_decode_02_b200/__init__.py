@@ -23,6 +23,7 @@ RSQ_GDN, RSQ_MAMBA2, RSQ_GLA, RSQ_KDA = 0, 1, 2, 3
 RSQ_RTN, RSQ_SR, RSQ_BDR, RSQ_SR_BDR = 0, 1, 2, 3
 RSQ_SR8, RSQ_SR8_BDR = 5, 7   # stochastic rounding with 8-bit uniforms (RSQ_SR: 16-bit)
 RSQ_F32, RSQ_BF16 = 0, 1
+RSQ_NORM_GATE, RSQ_GATE_NORM = 0, 1
 RSQ_OK, RSQ_E_INVAL, RSQ_E_UNSUPPORTED, RSQ_E_CUDA, RSQ_E_NOMEM, RSQ_E_NONFINITE = range(6)
 RSQ_MAX_HEADS = 512
 
@@ -71,11 +72,40 @@ class rsq_diag_inputs(ctypes.Structure):
                 ("alpha", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
 
 
+class rsq_scan_config(ctypes.Structure):
+    _fields_ = [("family", ctypes.c_int), ("in_dtype", ctypes.c_int), ("sequences", ctypes.c_int),
+                ("heads", ctypes.c_int), ("dk", ctypes.c_int), ("dv", ctypes.c_int),
+                ("ngroups", ctypes.c_int), ("ragged", ctypes.c_int), ("tokens", ctypes.c_int64)]
+
+
+class rsq_scan_inputs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("Bm", ctypes.c_void_p), ("Cm", ctypes.c_void_p),
+                ("dt", ctypes.c_void_p), ("A", ctypes.c_void_p), ("D", ctypes.c_void_p),
+                ("decay", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("b_stride", ctypes.c_int64), ("c_stride", ctypes.c_int64)]
+
+
+class rsq_scan_grads(ctypes.Structure):
+    _fields_ = [("dx", ctypes.c_void_p), ("dBm", ctypes.c_void_p), ("dCm", ctypes.c_void_p),
+                ("ddt", ctypes.c_void_p), ("dlog_decay", ctypes.c_void_p), ("dA", ctypes.c_void_p),
+                ("dD", ctypes.c_void_p), ("dstate_in", ctypes.c_void_p)]
+
+
+class rsq_norm_config(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int), ("group", ctypes.c_int),
+                ("order", ctypes.c_int), ("x_dtype", ctypes.c_int), ("side_dtype", ctypes.c_int),
+                ("y_dtype", ctypes.c_int), ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64),
+                ("side_stride", ctypes.c_int64)]
+
+
 _EXPORTS = ["rsq_create", "rsq_destroy", "rsq_state_bytes", "rsq_head_offset", "rsq_decode_step",
             "rsq_quantize", "rsq_dequantize", "rsq_state_drift", "rsq_check_flags",
             "rsq_allocate_bits", "rsq_reduction_partials", "rsq_status_string", "rsq_last_error",
             "rsq_version", "rsq_decode_step_noalloc", "rsq_decode_step_copy_scale",
-            "rsq_column_absmax", "rsq_window_bytes", "rsq_decode_step_window", "rsq_debug_waits"]
+            "rsq_column_absmax", "rsq_window_bytes", "rsq_decode_step_window", "rsq_debug_waits",
+            "rsq_scan_workspace", "rsq_scan", "rsq_scan_backward", "rsq_norm_workspace",
+            "rsq_gated_norm", "rsq_gated_norm_backward", "rsq_residual_norm",
+            "rsq_residual_norm_backward"]
 
 
 def _load():
@@ -118,6 +148,16 @@ def _load():
         "rsq_pipe_sync": ([P], C),
         "rsq_pipe_streams": ([P, ctypes.POINTER(P), ctypes.POINTER(P), ctypes.POINTER(P)], C),
         "rsq_debug_waits": ([P, ctypes.c_uint32, C], C),
+        "rsq_scan_workspace": ([ctypes.POINTER(rsq_scan_config), C, ctypes.POINTER(ctypes.c_size_t)], C),
+        "rsq_scan": ([ctypes.POINTER(rsq_scan_config), ctypes.POINTER(rsq_scan_inputs), P, P, P, P, P,
+                      ctypes.c_size_t, P], C),
+        "rsq_scan_backward": ([ctypes.POINTER(rsq_scan_config), ctypes.POINTER(rsq_scan_inputs), P, P, P, P,
+                               ctypes.POINTER(rsq_scan_grads), P, ctypes.c_size_t, P], C),
+        "rsq_norm_workspace": ([ctypes.POINTER(rsq_norm_config), ctypes.POINTER(ctypes.c_size_t)], C),
+        "rsq_gated_norm": ([ctypes.POINTER(rsq_norm_config)] + [P] * 5, C),
+        "rsq_gated_norm_backward": ([ctypes.POINTER(rsq_norm_config)] + [P] * 8 + [ctypes.c_size_t, P], C),
+        "rsq_residual_norm": ([ctypes.POINTER(rsq_norm_config)] + [P] * 7, C),
+        "rsq_residual_norm_backward": ([ctypes.POINTER(rsq_norm_config)] + [P] * 11 + [ctypes.c_size_t, P], C),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -165,6 +205,33 @@ def _dptr(t) -> int | None:
     if not t.is_contiguous():
         raise ValueError("expected a contiguous CUDA tensor")
     return int(t.data_ptr())
+
+
+def _dptr_rows(t) -> int | None:
+    """As _dptr, for an argument whose rows may lie apart: only its last dimension
+    has to be contiguous."""
+    if t is None or isinstance(t, int) or not hasattr(t, "data_ptr") or not getattr(t, "is_cuda", False):
+        return _dptr(t)
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("expected a CUDA tensor with a contiguous last dimension")
+    return int(t.data_ptr())
+
+
+def _workspace(t) -> tuple[int | None, int]:
+    if t is None:
+        return None, 0
+    return _dptr(t), t.numel() * t.element_size()
+
+
+def _dtype_of(t) -> int:
+    """rsq_dtype of a tensor or a torch dtype."""
+    import torch
+    d = t if isinstance(t, torch.dtype) else t.dtype
+    if d == torch.float32:
+        return RSQ_F32
+    if d == torch.bfloat16:
+        return RSQ_BF16
+    raise ValueError("expected float32 or bfloat16, got %s" % d)
 
 
 def _hptr(t) -> int:
@@ -381,6 +448,58 @@ def rsq_reduction_partials(dk: int) -> int:
     return int(lib.rsq_reduction_partials(int(dk)))
 
 
+def rsq_scan_workspace(cfg: rsq_scan_config, backward: bool = False) -> int:
+    n = ctypes.c_size_t()
+    _check(lib.rsq_scan_workspace(ctypes.byref(cfg), int(backward), ctypes.byref(n)))
+    return int(n.value)
+
+
+def rsq_scan(cfg: rsq_scan_config, inputs: rsq_scan_inputs, out, *, cu_seqlens=None, state_in=None,
+             state_out=None, workspace=None, stream=None) -> None:
+    ws, n = _workspace(workspace)
+    _check(lib.rsq_scan(ctypes.byref(cfg), ctypes.byref(inputs), _dptr(cu_seqlens), _dptr(state_in),
+                        _dptr(state_out), _dptr(out), ws, n, _stream(stream)))
+
+
+def rsq_scan_backward(cfg: rsq_scan_config, inputs: rsq_scan_inputs, dout, grads: rsq_scan_grads, *,
+                      cu_seqlens=None, state_in=None, dstate_out=None, workspace=None, stream=None) -> None:
+    ws, n = _workspace(workspace)
+    _check(lib.rsq_scan_backward(ctypes.byref(cfg), ctypes.byref(inputs), _dptr(cu_seqlens), _dptr(state_in),
+                                 _dptr(dout), _dptr(dstate_out), ctypes.byref(grads), ws, n, _stream(stream)))
+
+
+def rsq_norm_workspace(cfg: rsq_norm_config) -> int:
+    n = ctypes.c_size_t()
+    _check(lib.rsq_norm_workspace(ctypes.byref(cfg), ctypes.byref(n)))
+    return int(n.value)
+
+
+def rsq_gated_norm(cfg: rsq_norm_config, x, z, w, y, stream=None) -> None:
+    """x and z may be row-strided (norm_config reads their strides)."""
+    _check(lib.rsq_gated_norm(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(z), _dptr(w), _dptr(y),
+                              _stream(stream)))
+
+
+def rsq_gated_norm_backward(cfg: rsq_norm_config, x, z, w, dy, dx, dz, dw, workspace=None, stream=None) -> None:
+    ws, n = _workspace(workspace)
+    _check(lib.rsq_gated_norm_backward(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(z), _dptr(w), _dptr(dy),
+                                       _dptr(dx), _dptr(dz), _dptr(dw), ws, n, _stream(stream)))
+
+
+def rsq_residual_norm(cfg: rsq_norm_config, x, residual, scale, w, h, y, stream=None) -> None:
+    """x and residual may be row-strided (norm_config reads their strides)."""
+    _check(lib.rsq_residual_norm(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(residual), _dptr(scale), _dptr(w),
+                                 _dptr(h), _dptr(y), _stream(stream)))
+
+
+def rsq_residual_norm_backward(cfg: rsq_norm_config, x, h, scale, w, dy, dh, dx, dresidual, dscale, dw,
+                               workspace=None, stream=None) -> None:
+    ws, n = _workspace(workspace)
+    _check(lib.rsq_residual_norm_backward(ctypes.byref(cfg), _dptr_rows(x), _dptr(h), _dptr(scale), _dptr(w),
+                                          _dptr(dy), _dptr(dh), _dptr(dx), _dptr(dresidual), _dptr(dscale),
+                                          _dptr(dw), ws, n, _stream(stream)))
+
+
 def rsq_version() -> str:
     return lib.rsq_version().decode()
 
@@ -415,6 +534,72 @@ def diag_inputs(q, k, v, alpha, beta=None) -> rsq_diag_inputs:
 
 def mamba2_inputs(x, Bm, Cm, dt, A, D, decay=None) -> rsq_mamba2_inputs:
     return rsq_mamba2_inputs(_dptr(x), _dptr(Bm), _dptr(Cm), _dptr(dt), _dptr(A), _dptr(D), _dptr(decay))
+
+
+def _token_rows(t, what: str) -> tuple[int | None, int]:
+    """Address and token stride of a [tokens, ...] argument whose token rows are packed
+    but may lie apart (a slice of a projection's output)."""
+    if t is None or isinstance(t, int):
+        return t, 0
+    inner = 1
+    for d in range(t.dim() - 1, 0, -1):
+        if t.shape[d] > 1 and t.stride(d) != inner:
+            raise ValueError("%s: the row of one token has to be contiguous" % what)
+        inner *= t.shape[d]
+    p = _dptr(t) if t.dim() < 2 or t.is_contiguous() else _dptr(t[:1].view(-1)) if t.shape[0] else _dptr(t[:1])
+    return p, int(t.stride(0)) if t.dim() > 1 and t.shape[0] > 1 else 0
+
+
+def scan_inputs(x, Bm, Cm, dt=None, A=None, D=None, decay=None) -> rsq_scan_inputs:
+    """x [tokens, heads, dv], Bm, Cm [tokens, ngroups, dk]: their tokens may lie apart."""
+    (xp, xs), (bp, bs), (cp, cs) = _token_rows(x, "x"), _token_rows(Bm, "Bm"), _token_rows(Cm, "Cm")
+    return rsq_scan_inputs(xp, bp, cp, _dptr(dt), _dptr(A), _dptr(D), _dptr(decay), xs, bs, cs)
+
+
+def scan_grads(dx=None, dBm=None, dCm=None, ddt=None, dlog_decay=None, dA=None, dD=None,
+               dstate_in=None) -> rsq_scan_grads:
+    return rsq_scan_grads(_dptr(dx), _dptr(dBm), _dptr(dCm), _dptr(ddt), _dptr(dlog_decay), _dptr(dA),
+                          _dptr(dD), _dptr(dstate_in))
+
+
+def norm_config(x, side, y, *, group: int = 0, order: int = RSQ_NORM_GATE, eps: float = 1e-5) -> rsq_norm_config:
+    """From the tensors of the call: x [rows, width], side (the gate z, or the residual
+    stream; None: no gate) of the same shape, y a tensor or a torch dtype."""
+    rows, width = x.shape
+    if side is not None and tuple(side.shape) != (rows, width):
+        raise ValueError("x has shape %s, the other input %s" % (tuple(x.shape), tuple(side.shape)))
+
+    def stride(t):
+        return int(t.stride(0)) if t is not None and rows > 1 else 0
+    return rsq_norm_config(rows, width, int(group), int(order), _dtype_of(x),
+                           RSQ_F32 if side is None else _dtype_of(side), _dtype_of(y), float(eps), stride(x),
+                           stride(side))
+
+
+class Scan:
+    """The scan of one layer over sequences of given total length (rsq_scan)."""
+
+    def __init__(self, sequences: int, tokens: int, heads: int, dk: int, dv: int, *, ngroups: int = 1,
+                 ragged: bool = False, family: int = RSQ_MAMBA2, in_dtype: int = RSQ_BF16):
+        self.cfg = rsq_scan_config(int(family), int(in_dtype), int(sequences), int(heads), int(dk), int(dv),
+                                   int(ngroups), int(ragged), int(tokens))
+        self.workspace_bytes = rsq_scan_workspace(self.cfg, False)
+        self.backward_workspace_bytes = rsq_scan_workspace(self.cfg, True)
+
+    def alloc_workspace(self, backward: bool = False, device="cuda"):
+        """One call's scratch (forward, or backward); calls that may overlap need one each."""
+        import torch
+        n = self.backward_workspace_bytes if backward else self.workspace_bytes
+        return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+    def forward(self, inputs, out, *, state_in=None, state_out=None, cu_seqlens=None, workspace=None, stream=None):
+        rsq_scan(self.cfg, inputs, out, cu_seqlens=cu_seqlens, state_in=state_in, state_out=state_out,
+                 workspace=workspace, stream=stream)
+
+    def backward(self, inputs, dout, grads, *, state_in=None, dstate_out=None, cu_seqlens=None, workspace=None,
+                 stream=None):
+        rsq_scan_backward(self.cfg, inputs, dout, grads, cu_seqlens=cu_seqlens, state_in=state_in,
+                          dstate_out=dstate_out, workspace=workspace, stream=stream)
 
 
 class Context:

@@ -145,6 +145,15 @@ rsq_status check_state(const rsq_ctx* c, const rsq_state* s, const char* name) {
 
 }  // namespace
 
+// The same record for the entry points of other translation units.
+rsq_status rsq::set_error(rsq_status s, const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof(g_err), fmt, ap);
+    va_end(ap);
+    return s;
+}
+
 extern "C" {
 
 rsq_status rsq_debug_waits(rsq_ctx* ctx, uint32_t wait_iters, int withhold) {

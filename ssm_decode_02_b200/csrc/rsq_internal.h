@@ -138,4 +138,8 @@ int decode_ka_info(int dk, int dv, int rnd, int* threads, size_t* smem, const vo
 int launch_quantize_ka(int dk, const QuantParams& p, void* stream);
 int launch_drift(const DriftParams& p, void* stream);
 
+
+// Records the calling thread's rsq_last_error text and returns `s`.
+rsq_status set_error(rsq_status s, const char* fmt, ...);
+
 }  // namespace rsq

@@ -1,0 +1,230 @@
+// scan_api.cu -- rsq_scan and rsq_scan_backward: validation, the workspace and the
+// order of the launches.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "scan.cuh"
+
+namespace rsq {
+namespace scan {
+namespace {
+
+constexpr int kSms = 148;
+constexpr int64_t kMaxTokens = (1LL << 31) - (1LL << 17);
+// Longest sequences (equal lengths) that the token-by-token kernel takes.
+constexpr int kStepTokens = 4;
+
+bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128 || d == 256; }
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+// gates, their gradients and bounds are read and written one at a time
+bool odd_float(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+rsq_status check_config(const char* who, const rsq_scan_config* c) {
+    if (!c) return set_error(RSQ_E_INVAL, "%s: null config", who);
+    if (c->family < RSQ_GDN || c->family > RSQ_KDA) return set_error(RSQ_E_INVAL, "%s: bad family %d", who, c->family);
+    if (c->family != RSQ_MAMBA2)
+        return set_error(RSQ_E_UNSUPPORTED, "%s: built for the scalar-decay family (RSQ_MAMBA2)", who);
+    if (c->in_dtype != RSQ_F32 && c->in_dtype != RSQ_BF16) return set_error(RSQ_E_INVAL, "%s: bad in_dtype %d", who, c->in_dtype);
+    if (c->in_dtype != RSQ_BF16) return set_error(RSQ_E_UNSUPPORTED, "%s: built for bf16 inputs", who);
+    if (c->sequences < 1 || c->sequences > 65536) return set_error(RSQ_E_INVAL, "%s: sequences must be in [1, 65536]", who);
+    if (c->heads < 1 || c->heads > RSQ_MAX_HEADS) return set_error(RSQ_E_INVAL, "%s: heads must be in [1, %d]", who, RSQ_MAX_HEADS);
+    if (!dim_ok(c->dk) || !dim_ok(c->dv))
+        return set_error(RSQ_E_UNSUPPORTED, "%s: dk and dv must be one of 16, 32, 64, 128, 256 (got %d, %d)", who, c->dk, c->dv);
+    if (c->ngroups < 1 || c->heads % c->ngroups) return set_error(RSQ_E_INVAL, "%s: ngroups must divide heads", who);
+    if (c->ragged != 0 && c->ragged != 1) return set_error(RSQ_E_INVAL, "%s: ragged must be 0 or 1", who);
+    if (c->tokens < 0 || c->tokens > kMaxTokens) return set_error(RSQ_E_INVAL, "%s: tokens out of range", who);
+    if (!c->ragged && c->tokens % c->sequences)
+        return set_error(RSQ_E_INVAL, "%s: tokens must be a multiple of sequences (or ragged)", who);
+    return RSQ_OK;
+}
+
+bool takes_steps(const rsq_scan_config& c) { return !c.ragged && c.tokens / c.sequences <= kStepTokens; }
+
+// Sizes and the workspace's layout, offsets from `base` (null: to count bytes).
+size_t layout(const rsq_scan_config& c, bool backward, Params* p, uint8_t* base) {
+    p->n = c.sequences;
+    p->H = c.heads;
+    p->N = c.dk;
+    p->P = c.dv;
+    p->G = c.ngroups;
+    p->per = c.heads / c.ngroups;
+    p->tiles = (c.dv + kTile - 1) / kTile;
+    p->ragged = c.ragged;
+    p->tokens = static_cast<int>(c.tokens);
+    p->len = c.ragged ? 0 : static_cast<int>(c.tokens / c.sequences);
+    auto slots_of = [&](int unit) {
+        return c.ragged ? p->tokens / unit + p->n : p->n * ((p->len + unit - 1) / unit);
+    };
+    p->slots = slots_of(kChunk);
+    // Segments where the sequences alone leave SMs idle: twice the work on the
+    // states for as many more blocks.
+    const long long blocks = static_cast<long long>(p->n) * p->H * p->tiles * (backward ? 2 : 1);
+    const int chunks = p->slots / p->n;
+    p->seg_chunks = 0;
+    if (blocks * 4 <= 2 * kSms && chunks >= 16) {
+        const int want = static_cast<int>((2 * kSms + blocks - 1) / blocks);
+        p->seg_chunks = std::max(4, (chunks + want - 1) / want);
+        if (p->seg_chunks * 2 > chunks) p->seg_chunks = 0;
+    }
+    p->seg_slots = p->seg_chunks ? slots_of(kChunk * p->seg_chunks) : 0;
+
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t* q = base ? base + at : nullptr;
+        at += (bytes + 255) / 256 * 256;
+        return q;
+    };
+    const size_t cells = static_cast<size_t>(p->slots) * p->H;
+    const size_t state = static_cast<size_t>(p->N) * kTile * p->tiles;
+    p->gb = reinterpret_cast<float2*>(take(cells * kChunk * sizeof(float2)));
+    p->gdt = reinterpret_cast<float*>(take(cells * kChunk * sizeof(float)));
+    if (backward) {
+        p->sf = reinterpret_cast<float*>(take(cells * state * sizeof(float)));
+        p->df = reinterpret_cast<float*>(take(cells * state * sizeof(float)));
+        p->part = reinterpret_cast<float*>(take(2 * cells * sizeof(float)));
+    } else {
+        p->sh = reinterpret_cast<bf16*>(take(cells * state * sizeof(bf16)));
+    }
+    if (p->seg_chunks) {
+        const size_t n = static_cast<size_t>(p->seg_slots) * p->H;
+        for (int d = 0; d < (backward ? 2 : 1); ++d) {
+            p->seg_end[d] = reinterpret_cast<float*>(take(n * p->N * p->P * sizeof(float)));
+            p->seg_start[d] = reinterpret_cast<float*>(take(n * p->N * p->P * sizeof(float)));
+        }
+        p->seg_log = reinterpret_cast<double*>(take(n * sizeof(double)));
+    }
+    return at;
+}
+
+rsq_status check_inputs(const char* who, const rsq_scan_config& c, const rsq_scan_inputs* in, const int32_t* cu, Params* p) {
+    if (!in) return set_error(RSQ_E_INVAL, "%s: null inputs", who);
+    const bool any = c.tokens > 0;
+    if (any && (!in->x || !in->Bm || !in->Cm)) return set_error(RSQ_E_INVAL, "%s: null x, Bm or Cm", who);
+    if (!in->decay && (!in->dt || !in->A)) return set_error(RSQ_E_INVAL, "%s: without decay, dt and A are needed", who);
+    if (c.ragged && !cu) return set_error(RSQ_E_INVAL, "%s: ragged needs cu_seqlens", who);
+    if (!c.ragged && cu) return set_error(RSQ_E_INVAL, "%s: cu_seqlens without ragged", who);
+    for (const void* q : {in->x, in->Bm, in->Cm})
+        if (misaligned(q)) return set_error(RSQ_E_INVAL, "%s: x, Bm or Cm is not 16-byte aligned", who);
+    for (const void* q : {static_cast<const void*>(in->dt), static_cast<const void*>(in->A), static_cast<const void*>(in->D),
+                          static_cast<const void*>(in->decay), static_cast<const void*>(cu)})
+        if (odd_float(q)) return set_error(RSQ_E_INVAL, "%s: a gate array or cu_seqlens is not 4-byte aligned", who);
+    const int64_t row[3] = {static_cast<int64_t>(c.heads) * c.dv, static_cast<int64_t>(c.ngroups) * c.dk,
+                            static_cast<int64_t>(c.ngroups) * c.dk};
+    const int64_t given[3] = {in->x_stride, in->b_stride, in->c_stride};
+    long long* out[3] = {&p->xs, &p->bs, &p->cs};
+    for (int i = 0; i < 3; ++i) {
+        *out[i] = given[i] ? given[i] : row[i];
+        if (*out[i] < row[i] || *out[i] % 8 || *out[i] > (1LL << 31))
+            return set_error(RSQ_E_INVAL, "%s: a token stride must be a multiple of 8, at least the row and at most 2^31", who);
+    }
+    p->x = static_cast<const bf16*>(in->x);
+    p->Bm = static_cast<const bf16*>(in->Bm);
+    p->Cm = static_cast<const bf16*>(in->Cm);
+    p->dt = in->dt;
+    p->A = in->A;
+    p->D = in->D;
+    p->decay = in->decay;
+    p->cu = cu;
+    return RSQ_OK;
+}
+
+rsq_status check_workspace(const char* who, size_t need, const void* ws, size_t bytes) {
+    if (!need) return RSQ_OK;
+    if (!ws || misaligned(ws)) return set_error(RSQ_E_INVAL, "%s: workspace null or not 16-byte aligned", who);
+    if (bytes < need) return set_error(RSQ_E_INVAL, "%s: workspace of %zu bytes, %zu needed", who, bytes, need);
+    return RSQ_OK;
+}
+
+// Heads of a block of the chunk kernels: as many as share the scores' work and
+// still leave about four blocks per SM.
+int head_set(const Params& p) {
+    const long long all = static_cast<long long>(std::max(1, p.tokens / kChunk)) * p.H;
+    return static_cast<int>(std::max<long long>(1, std::min<long long>(p.per, all / (4 * kSms))));
+}
+
+rsq_status done(const char* who, int err) {
+    return err ? set_error(RSQ_E_CUDA, "%s: %s", who, cudaGetErrorString(static_cast<cudaError_t>(err))) : RSQ_OK;
+}
+
+}  // namespace
+}  // namespace scan
+}  // namespace rsq
+
+using namespace rsq;
+using namespace rsq::scan;
+
+extern "C" {
+
+rsq_status rsq_scan_workspace(const rsq_scan_config* cfg, int backward, size_t* bytes) {
+    if (!bytes) return set_error(RSQ_E_INVAL, "scan_workspace: null argument");
+    const rsq_status st = check_config("scan_workspace", cfg);
+    if (st) return st;
+    if (backward != 0 && backward != 1) return set_error(RSQ_E_INVAL, "scan_workspace: backward must be 0 or 1");
+    Params p{};
+    *bytes = !backward && takes_steps(*cfg) ? 0 : layout(*cfg, backward, &p, nullptr);
+    return RSQ_OK;
+}
+
+rsq_status rsq_scan(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs, const int32_t* cu_seqlens,
+                    const float* state_in, float* state_out, void* out, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+    rsq_status st = check_config("scan", cfg);
+    if (st) return st;
+    Params p{};
+    if ((st = check_inputs("scan", *cfg, inputs, cu_seqlens, &p))) return st;
+    if (cfg->tokens && !out) return set_error(RSQ_E_INVAL, "scan: null out");
+    if (misaligned(out) || misaligned(state_in) || misaligned(state_out))
+        return set_error(RSQ_E_INVAL, "scan: out or a state is not 16-byte aligned");
+    const bool steps = takes_steps(*cfg);
+    if (!steps && (st = check_workspace("scan", layout(*cfg, false, &p, nullptr), workspace, workspace_bytes))) return st;
+    layout(*cfg, false, &p, steps ? nullptr : static_cast<uint8_t*>(workspace));
+    p.state_in = state_in;
+    p.state_out = state_out;
+    p.out = static_cast<bf16*>(out);
+    auto s = static_cast<cudaStream_t>(stream);
+    if (steps) return done("scan", launch_step(p, s));
+    int err = p.slots ? launch_gates(p, s) : 0;
+    if (!err) err = launch_states(p, false, s);
+    if (!err && p.slots) err = launch_out(p, head_set(p), s);
+    return done("scan", err);
+}
+
+rsq_status rsq_scan_backward(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs, const int32_t* cu_seqlens,
+                             const float* state_in, const void* dout, const float* dstate_out,
+                             const rsq_scan_grads* grads, void* workspace, size_t workspace_bytes, void* stream) {
+    rsq_status st = check_config("scan_backward", cfg);
+    if (st) return st;
+    Params p{};
+    if ((st = check_inputs("scan_backward", *cfg, inputs, cu_seqlens, &p))) return st;
+    if (!grads) return set_error(RSQ_E_INVAL, "scan_backward: null grads");
+    if (cfg->tokens && !dout) return set_error(RSQ_E_INVAL, "scan_backward: null dout");
+    if (grads->dA && inputs->decay) return set_error(RSQ_E_INVAL, "scan_backward: dA with a given decay");
+    for (const void* q : {dout, static_cast<const void*>(state_in), static_cast<const void*>(dstate_out), static_cast<const void*>(grads->dx),
+                          static_cast<const void*>(grads->dBm), static_cast<const void*>(grads->dCm),
+                          static_cast<const void*>(grads->dstate_in)})
+        if (misaligned(q)) return set_error(RSQ_E_INVAL, "scan_backward: a buffer is not 16-byte aligned");
+    for (const void* q : {static_cast<const void*>(grads->ddt), static_cast<const void*>(grads->dlog_decay),
+                          static_cast<const void*>(grads->dA), static_cast<const void*>(grads->dD)})
+        if (odd_float(q)) return set_error(RSQ_E_INVAL, "scan_backward: a gate gradient is not 4-byte aligned");
+    if ((st = check_workspace("scan_backward", layout(*cfg, true, &p, nullptr), workspace, workspace_bytes))) return st;
+    layout(*cfg, true, &p, static_cast<uint8_t*>(workspace));
+    p.state_in = state_in;
+    p.dout = static_cast<const bf16*>(dout);
+    p.dstate_out = dstate_out;
+    p.dx = static_cast<bf16*>(grads->dx);
+    p.dBm = static_cast<bf16*>(grads->dBm);
+    p.dCm = static_cast<bf16*>(grads->dCm);
+    p.ddt = grads->ddt;
+    p.dlog = grads->dlog_decay;
+    p.dA = grads->dA;
+    p.dD = grads->dD;
+    p.dstate_in = grads->dstate_in;
+    auto s = static_cast<cudaStream_t>(stream);
+    int err = p.slots ? launch_gates(p, s) : 0;
+    if (!err) err = launch_states(p, true, s);
+    if (!err) err = launch_backward(p, head_set(p), s);
+    return done("scan_backward", err);
+}
+
+}  // extern "C"
