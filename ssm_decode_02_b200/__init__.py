@@ -249,10 +249,19 @@ def _hptr(t) -> int:
     return p
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            # the handle alone: torch.cuda.current_stream() builds an object around it, 3 us a call
+            _raw_stream = ((lambda: get(torch._C._cuda_getDevice())) if get and torch.cuda.is_initialized()
+                           else (lambda: int(torch.cuda.current_stream().cuda_stream)))
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)

@@ -23,10 +23,9 @@ namespace rsq {
 namespace {
 
 constexpr int kMaxThreads = 512;
+constexpr int kBackwardRegs = 96;
 constexpr int kMaxWidth = 16384;
-// Blocks over all groups: four per SM.  More blocks mean more partial sums to
-// add up in the backward pass, fewer leave HBM idle while a block reduces.
-constexpr int kBlocks = 592;
+constexpr int kForwardBlocks = 2368;  // over all groups: every thread an SM can hold, and a few rows each
 
 enum Mode { kPlain = 0, kNormGate = 1, kGateNorm = 2, kResidual = 3 };
 
@@ -35,7 +34,6 @@ struct NormParams {
     int width, group;
     int tpu, upb;                 // threads of a unit, rows a block takes at a time
     float eps;
-    int y_f32;
     long long xs, ss;             // row strides of x and of z / residual
     const void* x;
     const void* side;             // z | residual (forward) / h (backward)
@@ -131,8 +129,14 @@ __device__ __forceinline__ void load_cols(const float* p, float (&v)[VEC]) {
     for (int i = 0; i < VEC; ++i) v[i] = r.get(i);
 }
 
-// 1 / (1 + e^-z): e^-z = inf gives 0.
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + e^-z): e^-z = inf gives 0.  Flushing subnormals (.ftz) saves the scaling
+// around both approximations and changes no result by more than 2^-126.
+__device__ __forceinline__ float sigmoid(float z) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
 
 // Sums (a, b) over the unit's threads; every thread gets them.  Units of at
 // most a warp use shuffles among their lanes; a larger unit is a whole block.
@@ -141,259 +145,278 @@ __device__ __forceinline__ float2 unit_sum(float2 s, int tpu, float2* sh) {
         s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
         s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
     }
-    if (tpu > 32) {
-        if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+    if (tpu > 32) {  // at most 16 warps: every half-warp adds up their sums
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) sh[threadIdx.x >> 5] = s;
         __syncthreads();
-        s = make_float2(0.f, 0.f);
-        for (int i = 0; i < tpu / 32; ++i) {
-            s.x += sh[i].x;
-            s.y += sh[i].y;
+        s = (lane & 15) < tpu / 32 ? sh[lane & 15] : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int d = 8; d; d >>= 1) {
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
         }
     }
     return s;
 }
 
-template <class TX, class TS, int VEC, int K>
-struct RowRaw {
-    Raw<TX, VEC> x[K];
-    Raw<TS, VEC> s[K];
-};
+// A thread's part of one row of one array: K vectors, tpu vectors apart.
+template <class T, int VEC, int K>
+struct Part {
+    Raw<T, VEC> v[K];
 
-template <int MODE, class TX, class TS, int VEC, int K>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const __grid_constant__ NormParams p) {
-    __shared__ float2 sh[2][kMaxThreads / 32];
-    const int sub = threadIdx.x / p.tpu, t = threadIdx.x - sub * p.tpu;
-    const int g0 = blockIdx.y * p.group;
-    const TX* x = static_cast<const TX*>(p.x);
-    const TS* side = static_cast<const TS*>(p.side);
-    const bool has_side = MODE == kNormGate || MODE == kGateNorm || (MODE == kResidual && side);
-    const float inv_n = 1.f / static_cast<float>(p.group);
-
-    // the group's vectors that do not change from row to row
-    float w[K][VEC], sc[K][VEC];
-    bool on[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = (t + k * p.tpu) * VEC;
-        on[k] = c < p.group;
-        if (on[k]) load_cols<VEC>(p.w + g0 + c, w[k]);
-        if constexpr (MODE == kResidual) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) sc[k][i] = 1.f;
-            if (on[k] && p.scale) load_cols<VEC>(p.scale + g0 + c, sc[k]);
-        }
-    }
-    auto fetch = [&](long long row, RowRaw<TX, TS, VEC, K>& r) {
+    // `mine`: the thread's first vector, the others `apart` elements from one another; zero
+    // where not `on`
+    __device__ __forceinline__ void fetch(const T* mine, int apart, const bool (&on)[K], bool row_on) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (t + k * p.tpu) * VEC;
-            r.x[k].zero();
-            r.s[k].zero();
-            if (on[k] && row < p.rows) {
-                r.x[k].load(x + row * p.xs + g0 + c);
-                if (has_side) r.s[k].load(side + row * p.ss + g0 + c);
-            }
+            v[k].zero();
+            if (on[k] && row_on) v[k].load(mine + k * apart);
         }
-    };
-    const long long step = static_cast<long long>(gridDim.x) * p.upb;
-    RowRaw<TX, TS, VEC, K> next;
-    fetch(static_cast<long long>(blockIdx.x) * p.upb + sub, next);
+    }
+};
+
+template <int MODE, class TX, class TS, class TY, int VEC, int K>
+__global__ void __launch_bounds__(kMaxThreads) __maxnreg__(VEC * K <= 16 && VEC == 8 ? 48 : 128)
+norm_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float2 sh[2][kMaxThreads / 32];
+    const int sub = threadIdx.x / p.tpu, t = threadIdx.x - sub * p.tpu;
+    const int col = blockIdx.y * p.group + t * VEC, apart = p.tpu * VEC;
+    const float inv_n = 1.f / static_cast<float>(p.group);
+    bool on[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) on[k] = (t + k * p.tpu) * VEC < p.group;
+    const TX* x = static_cast<const TX*>(p.x);
+    const TS* side = static_cast<const TS*>(p.side);
     int buf = 0;
-    for (long long r0 = static_cast<long long>(blockIdx.x) * p.upb; r0 < p.rows; r0 += step, buf ^= 1) {
+    for (long long r0 = static_cast<long long>(blockIdx.x) * p.upb; r0 < p.rows; r0 += static_cast<long long>(gridDim.x) * p.upb, buf ^= 1) {
         const long long row = r0 + sub;
-        const RowRaw<TX, TS, VEC, K> cur = next;
-        fetch(row + step, next);
+        const bool row_on = row < p.rows;
+        Part<TX, VEC, K> xs;
+        Part<TS, VEC, K> ss;
+        xs.fetch(x + row * p.xs + col, apart, on, row_on);
+        if constexpr (MODE != kPlain) ss.fetch(side + row * p.ss + col, apart, on, row_on && side);
         float u[K][VEC];
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+            float sc[VEC];
+            if (MODE == kResidual && p.scale) {  // the same columns every row: from L1
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) sc[i] = 0.f;
+                if (on[k]) load_cols<VEC>(p.scale + col + k * apart, sc);
+            }
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                float v = cur.x[k].get(i);
+                float v = xs.v[k].get(i);
                 if constexpr (MODE == kGateNorm) {
-                    const float z = cur.s[k].get(i);
+                    const float z = ss.v[k].get(i);
                     v *= z * sigmoid(z);
                 }
                 if constexpr (MODE == kResidual) {
-                    v = fmaf(sc[k][i], v, cur.s[k].get(i));
+                    v = p.scale ? fmaf(sc[i], v, ss.v[k].get(i)) : v + ss.v[k].get(i);
                     // the norm is that of the residual stream as stored
                     if constexpr (sizeof(TS) == 2) v = __bfloat162float(__float2bfloat16_rn(v));
-                    if (!on[k]) v = 0.f;
                 }
                 u[k][i] = v;
                 sum = fmaf(v, v, sum);
             }
         }
         const float r = rsqrtf(fmaf(unit_sum(make_float2(sum, 0.f), p.tpu, sh[buf]).x, inv_n, p.eps));
-        if (row < p.rows) {
+        if (!row_on) continue;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (!on[k]) continue;
-                const long long at = row * p.width + g0 + (t + k * p.tpu) * VEC;
-                if constexpr (MODE == kResidual) store<VEC>(static_cast<TS*>(p.out2) + at, u[k]);
-                float o[VEC];
+        for (int k = 0; k < K; ++k) {
+            if (!on[k]) continue;
+            const long long at = row * p.width + col + k * apart;
+            if constexpr (MODE == kResidual) store<VEC>(static_cast<TS*>(p.out2) + at, u[k]);
+            float o[VEC], w[VEC];
+            load_cols<VEC>(p.w + col + k * apart, w);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    o[i] = u[k][i] * r * w[k][i];
-                    if constexpr (MODE == kNormGate) {
-                        const float z = cur.s[k].get(i);
-                        o[i] *= z * sigmoid(z);
-                    }
+            for (int i = 0; i < VEC; ++i) {
+                o[i] = u[k][i] * r * w[i];
+                if constexpr (MODE == kNormGate) {
+                    const float z = ss.v[k].get(i);
+                    o[i] *= z * sigmoid(z);
                 }
-                if (p.y_f32)
-                    store<VEC>(static_cast<float*>(p.y) + at, o);
-                else
-                    store<VEC>(static_cast<__nv_bfloat16*>(p.y) + at, o);
             }
+            store<VEC>(static_cast<TY*>(p.y) + at, o);
         }
     }
 }
 
-// Adds VEC values to a thread's own places of the shared column sums.  Sums of
-// VEC = 8 lie as two float4 planes so that a warp's accesses do not conflict.
+// A thread's own K vectors of a block's shared array, as pieces of four floats (VEC
+// = 8) that lie next to those of its neighbours.
 template <int VEC>
-__device__ __forceinline__ void add_cols(float* acc, int slot, int slots, const float (&v)[VEC]) {
-    if constexpr (VEC == 8) {
-        float4* a = reinterpret_cast<float4*>(acc);
-        float4 lo = a[slot], hi = a[slots + slot];
-        lo.x += v[0];
-        lo.y += v[1];
-        lo.z += v[2];
-        lo.w += v[3];
-        hi.x += v[4];
-        hi.y += v[5];
-        hi.z += v[6];
-        hi.w += v[7];
-        a[slot] = lo;
-        a[slots + slot] = hi;
-    } else {
-        acc[slot] += v[0];
+struct Own {
+    float* base;
+    __device__ __forceinline__ float* at(int piece) const { return base + (piece * blockDim.x + threadIdx.x) * (VEC == 8 ? 4 : 1); }
+    __device__ __forceinline__ void set(int k, const float (&v)[VEC]) const {
+        if constexpr (VEC == 8) {
+            *reinterpret_cast<float4*>(at(2 * k)) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(at(2 * k + 1)) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *at(k) = v[0];
+        }
     }
-}
+    __device__ __forceinline__ void get(int k, float (&v)[VEC]) const {
+        if constexpr (VEC == 8) {
+            const float4 a = *reinterpret_cast<const float4*>(at(2 * k)), b = *reinterpret_cast<const float4*>(at(2 * k + 1));
+            v[0] = a.x;
+            v[1] = a.y;
+            v[2] = a.z;
+            v[3] = a.w;
+            v[4] = b.x;
+            v[5] = b.y;
+            v[6] = b.z;
+            v[7] = b.w;
+        } else {
+            v[0] = *at(k);
+        }
+    }
+    __device__ __forceinline__ void add(int k, const float (&v)[VEC]) const {
+        float o[VEC];
+        get(k, o);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o[i] += v[i];
+        set(k, o);
+    }
+};
 
-template <int MODE, class TX, class TS, int VEC, int K>
-__global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const __grid_constant__ NormParams p) {
-    extern __shared__ float4 acc4[];   // column sums of dw, then of dscale: [K][threads] chunks each
+// Whether w and scale fit shared memory beside the column sums: up to 8192 columns.
+template <int VEC, int K>
+constexpr bool kKeepCols = VEC * K <= 16;
+
+// Backward.  Between the loads of a row and its stores lie two passes over its
+// elements and one reduction.  What bounds it is how many rows an SM can have in
+// that chain, so registers hold the row as loaded and its sigmoids alone, and the
+// second pass makes u and dn again; w, scale and the column sums lie in shared
+// memory at places of the thread's own.
+template <int MODE, class TX, class TS, class TY, int VEC, int K>
+__global__ void __launch_bounds__(kMaxThreads) __maxnreg__(VEC * K <= 16 && VEC == 8 ? kBackwardRegs : 128)
+norm_backward_kernel(const __grid_constant__ NormParams p) {
+    constexpr bool GATED = MODE == kNormGate || MODE == kGateNorm;
+    constexpr bool KEEP = kKeepCols<VEC, K>;
+    extern __shared__ float4 own4[];  // sums of dw, of dscale (if wanted), w, scale: [K][threads] vectors each
     __shared__ float2 sh[2][kMaxThreads / 32];
-    float* acc = reinterpret_cast<float*>(acc4);
-    const int slots = K * blockDim.x;
-    float* acc_s = acc + slots * VEC;
+    const int floats = K * VEC * blockDim.x;
+    const Own<VEC> acc{reinterpret_cast<float*>(own4)}, acc_s{acc.base + floats}, ws{acc_s.base + (p.part_s ? floats : 0)},
+        scales{ws.base + floats};
     const int sub = threadIdx.x / p.tpu, t = threadIdx.x - sub * p.tpu;
-    const int g0 = blockIdx.y * p.group;
+    const int g0 = blockIdx.y * p.group, col = g0 + t * VEC, apart = p.tpu * VEC;
+    const float inv_n = 1.f / static_cast<float>(p.group);
+    const bool want_s = MODE == kResidual && p.part_s;
     const TX* x = static_cast<const TX*>(p.x);
     const TS* side = static_cast<const TS*>(p.side);
     const TS* dh = static_cast<const TS*>(p.dh);
-    const float inv_n = 1.f / static_cast<float>(p.group);
-    const bool want_s = MODE == kResidual && p.part_s;
-    const bool need_x = MODE != kResidual || want_s;
-
-    for (int i = threadIdx.x; i < slots * VEC * (want_s ? 2 : 1); i += blockDim.x) acc[i] = 0.f;
-    __syncthreads();
-
-    struct Row {
-        Raw<TX, VEC> x[K];
-        Raw<TS, VEC> s[K];
-        Raw<__nv_bfloat16, VEC> d[K];
-        Raw<float, VEC> df[K];
-        Raw<TS, VEC> dh[K];
-    };
-    auto fetch = [&](long long row, Row& r) {
+    bool on[K];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (t + k * p.tpu) * VEC;
-            r.x[k].zero();
-            r.s[k].zero();
-            r.d[k].zero();
-            r.df[k].zero();
-            r.dh[k].zero();
-            if (c >= p.group || row >= p.rows) continue;
-            const long long at = row * p.width + g0 + c;
-            if (need_x) r.x[k].load(x + row * p.xs + g0 + c);
-            if (MODE != kPlain) r.s[k].load(side + row * p.ss + g0 + c);
-            if (p.y_f32)
-                r.df[k].load(static_cast<const float*>(p.dy) + at);
-            else
-                r.d[k].load(static_cast<const __nv_bfloat16*>(p.dy) + at);
-            if (MODE == kResidual && dh) r.dh[k].load(dh + at);
+    for (int k = 0; k < K; ++k) {
+        on[k] = (t + k * p.tpu) * VEC < p.group;
+        float v[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = 0.f;
+        acc.set(k, v);
+        if (want_s) acc_s.set(k, v);
+        if constexpr (KEEP) {
+            if (on[k]) load_cols<VEC>(p.w + col + k * apart, v);
+            ws.set(k, v);
+            if (MODE == kResidual && p.scale) {
+                if (on[k]) load_cols<VEC>(p.scale + col + k * apart, v);
+                scales.set(k, v);
+            }
+        }
+    }
+    auto weights = [&](int k, float (&v)[VEC]) {
+        if constexpr (KEEP) {
+            ws.get(k, v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = 0.f;
+            if (on[k]) load_cols<VEC>(p.w + col + k * apart, v);
         }
     };
-    const long long step = static_cast<long long>(gridDim.x) * p.upb;
-    Row cur;
     int buf = 0;
-    for (long long r0 = static_cast<long long>(blockIdx.x) * p.upb; r0 < p.rows; r0 += step, buf ^= 1) {
-        const long long row = r0 + sub;
-        fetch(row, cur);
+    for (long long r0 = static_cast<long long>(blockIdx.x) * p.upb; r0 < p.rows; r0 += static_cast<long long>(gridDim.x) * p.upb, buf ^= 1) {
+        const long long row = r0 + sub, packed = row * p.width + col;
+        const bool row_on = row < p.rows;
+        Part<TX, VEC, K> xs;
+        Part<TS, VEC, K> ss, hs;
+        Part<TY, VEC, K> ys;
+        ys.fetch(static_cast<const TY*>(p.dy) + packed, apart, on, row_on);
+        if (MODE != kResidual || want_s) xs.fetch(x + row * p.xs + col, apart, on, row_on);
+        if constexpr (MODE != kPlain) ss.fetch(side + row * p.ss + col, apart, on, row_on);
+        if constexpr (MODE == kResidual) hs.fetch(dh + packed, apart, on, row_on && dh);
+
+        float sg[K][VEC], w[VEC] = {};
         // u: what is normed; dn: the gradient of n
-        float u[K][VEC], dn[K][VEC];
+        auto u_dn = [&](int k, int i, float& u, float& dn) {
+            dn = ys.v[k].get(i) * w[i];
+            if constexpr (MODE == kResidual)
+                u = ss.v[k].get(i);
+            else
+                u = xs.v[k].get(i);
+            if constexpr (MODE == kGateNorm) u *= ss.v[k].get(i) * sg[k][i];
+            if constexpr (MODE == kNormGate) dn *= ss.v[k].get(i) * sg[k][i];
+        };
         float su = 0.f, sd = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (t + k * p.tpu) * VEC;
-            float w[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) w[i] = 0.f;
-            if (c < p.group) load_cols<VEC>(p.w + g0 + c, w);
+            weights(k, w);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float dy = p.y_f32 ? cur.df[k].get(i) : cur.d[k].get(i);
-                float v = MODE == kResidual ? cur.s[k].get(i) : cur.x[k].get(i);
-                float d = dy * w[i];
-                if constexpr (MODE == kNormGate || MODE == kGateNorm) {
-                    const float z = cur.s[k].get(i);
-                    const float gate = z * sigmoid(z);
-                    if constexpr (MODE == kGateNorm) v *= gate;
-                    if constexpr (MODE == kNormGate) d *= gate;
-                }
-                u[k][i] = v;
-                dn[k][i] = d;
-                su = fmaf(v, v, su);
-                sd = fmaf(d, v, sd);
+                if constexpr (GATED) sg[k][i] = sigmoid(ss.v[k].get(i));
+                float u, dn;
+                u_dn(k, i, u, dn);
+                su = fmaf(u, u, su);
+                sd = fmaf(dn, u, sd);
             }
         }
         const float2 s = unit_sum(make_float2(su, sd), p.tpu, sh[buf]);
         const float r = rsqrtf(fmaf(s.x, inv_n, p.eps));
-        const float m = s.y * r * inv_n;
-        if (row >= p.rows) continue;
+        if (!row_on) continue;
+        const float m = -s.y * r * r * inv_n;  // du = r dn + r m u
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (t + k * p.tpu) * VEC;
-            if (c >= p.group) continue;
-            const long long at = row * p.width + g0 + c;
-            float dx[VEC], d2[VEC], dw[VEC], w[VEC];
-            load_cols<VEC>((MODE == kResidual && p.scale ? p.scale : p.w) + g0 + c, w);
+            float dx[VEC], d2[VEC], dw[VEC], sc[VEC];
+            weights(k, w);
+            if (MODE == kResidual && p.scale) {
+                if constexpr (KEEP)
+                    scales.get(k, sc);
+                else if (on[k])
+                    load_cols<VEC>(p.scale + col + k * apart, sc);
+            }
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                const float dy = p.y_f32 ? cur.df[k].get(i) : cur.d[k].get(i);
-                const float n = u[k][i] * r;
-                const float du = r * fmaf(-n, m, dn[k][i]);
+                float u, dn;
+                u_dn(k, i, u, dn);
+                const float du = r * fmaf(u, m, dn);
+                const float gn = ys.v[k].get(i) * u * r;
                 dx[i] = du;
                 d2[i] = 0.f;
-                dw[i] = dy * n;
-                if constexpr (MODE == kNormGate || MODE == kGateNorm) {
-                    const float z = cur.s[k].get(i), sg = sigmoid(z), gate = z * sg;
-                    const float slope = sg * fmaf(z, 1.f - sg, 1.f);
+                dw[i] = gn;
+                if constexpr (GATED) {
+                    const float z = ss.v[k].get(i), gate = z * sg[k][i];
+                    const float slope = sg[k][i] * fmaf(z, 1.f - sg[k][i], 1.f);
                     if constexpr (MODE == kGateNorm) {
+                        d2[i] = du * xs.v[k].get(i) * slope;
                         dx[i] = du * gate;
-                        d2[i] = du * cur.x[k].get(i) * slope;
                     } else {
-                        d2[i] = dy * n * w[i] * slope;
-                        dw[i] *= gate;
+                        d2[i] = gn * w[i] * slope;
+                        dw[i] = gn * gate;
                     }
                 }
                 if constexpr (MODE == kResidual) {
-                    d2[i] = du + cur.dh[k].get(i);
-                    dx[i] = p.scale ? d2[i] * w[i] : d2[i];
+                    d2[i] = du + hs.v[k].get(i);
+                    dx[i] = p.scale ? d2[i] * sc[i] : d2[i];
                 }
             }
-            if (p.y) store<VEC>(static_cast<TX*>(p.y) + at, dx);
-            if (MODE != kPlain && p.out2) store<VEC>(static_cast<TS*>(p.out2) + at, d2);
-            const int slot = k * blockDim.x + threadIdx.x;
-            if (p.part_w) add_cols<VEC>(acc, slot, slots, dw);
+            if (!on[k]) continue;
+            if (p.y) store<VEC>(static_cast<TX*>(p.y) + packed + k * apart, dx);
+            if (MODE != kPlain && p.out2) store<VEC>(static_cast<TS*>(p.out2) + packed + k * apart, d2);
+            if (p.part_w) acc.add(k, dw);
             if (want_s) {
-                float ds[VEC];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) ds[i] = d2[i] * cur.x[k].get(i);
-                add_cols<VEC>(acc_s, slot, slots, ds);
+                for (int i = 0; i < VEC; ++i) d2[i] *= xs.v[k].get(i);
+                acc_s.add(k, d2);
             }
         }
     }
@@ -402,32 +425,36 @@ __global__ void __launch_bounds__(kMaxThreads) norm_backward_kernel(const __grid
     for (int which = 0; which < 2; ++which) {
         float* part = which ? p.part_s : p.part_w;
         if (!part || (which && !want_s)) continue;
-        const float* a = which ? acc_s : acc;
+        const float* a = which ? acc_s.base : acc.base;
         for (int c = threadIdx.x; c < p.group; c += blockDim.x) {
-            const int chunk = c / VEC, e = c - chunk * VEC;
-            const int k = chunk / p.tpu, tt = chunk - k * p.tpu;
+            const int vec = c / VEC, e = c - vec * VEC;
+            const int k = vec / p.tpu, tt = vec - k * p.tpu;
             float sum = 0.f;
             for (int q = 0; q < p.upb; ++q) {
-                const int slot = k * blockDim.x + q * p.tpu + tt;
-                sum += VEC == 8 ? a[((e >> 2) * slots + slot) * 4 + (e & 3)] : a[slot];
+                const int thread = q * p.tpu + tt;
+                sum += VEC == 8 ? a[((2 * k + (e >> 2)) * blockDim.x + thread) * 4 + (e & 3)] : a[k * blockDim.x + thread];
             }
             part[static_cast<long long>(blockIdx.x) * p.width + g0 + c] = sum;
         }
     }
 }
 
-// dw[c] = sum over the blocks' partial sums, in block order within each of 8
-// interleaved runs, the runs in order.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* part, int parts, int width, float* out) {
-    __shared__ float sh[8][33];
-    const int c = blockIdx.x * 32 + (threadIdx.x & 31), q = threadIdx.x >> 5;
+// out[c] = sum over the blocks' partial sums: 32 interleaved runs in block order,
+// then the runs in order.  blockIdx.y: dw, dscale.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* part_w, const float* part_s, int parts, int width,
+                                                          float* out_w, float* out_s) {
+    __shared__ float sh[32][33];
+    const float* part = blockIdx.y ? part_s : part_w;
+    float* out = blockIdx.y ? out_s : out_w;
+    if (!out) return;
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < width)
-        for (int i = q; i < parts; i += 8) s += part[static_cast<long long>(i) * width + c];
-    sh[q][threadIdx.x & 31] = s;
+        for (int i = q; i < parts; i += 32) s += __ldg(part + static_cast<long long>(i) * width + c);
+    sh[q][lane] = s;
     __syncthreads();
     if (q == 0 && c < width) {
-        for (int i = 1; i < 8; ++i) s += sh[i][threadIdx.x];
+        for (int i = 1; i < 32; ++i) s += sh[i][lane];
         out[c] = s;
     }
 }
@@ -436,12 +463,14 @@ struct Geometry {
     int vec, k, tpu, upb, gx;
 };
 
+// Backward blocks of an SM: those that fit at once (registers), four at most.
+int blocks_fit(const Geometry& g) { return std::max(1, std::min(4, 65536 / (kBackwardRegs * g.tpu * g.upb))); }
+
 // Vectors of eight elements where every row of every array starts on one
 // (width, group and strides multiples of 8; the bases are 16-byte aligned),
-// else single elements.  Two vectors per thread up to groups of 8192, so that
-// a thread has two loads of each input in flight and a backward row stays in
-// registers; four above.
-Geometry geometry(const rsq_norm_config& c) {
+// else single elements.  Two vectors per thread up to groups of 8192, four above:
+// one would leave half the threads of a block of 512 without work at 5120 columns.
+Geometry geometry(const rsq_norm_config& c, bool backward) {
     Geometry g;
     const bool wide = c.group % 8 == 0 && c.width % 8 == 0 && c.x_stride % 8 == 0 && c.side_stride % 8 == 0;
     g.vec = wide ? 8 : 1;
@@ -456,46 +485,55 @@ Geometry geometry(const rsq_norm_config& c) {
     g.upb = g.tpu <= 32 ? 128 / g.tpu : 1;
     const int groups = c.width / c.group;
     const long long blocks = (c.rows + g.upb - 1) / g.upb;
-    g.gx = static_cast<int>(std::max<long long>(1, std::min<long long>(blocks, std::max(1, kBlocks / groups))));
+    // Backward: the blocks that fit at once, so that none waits with its whole share
+    // of rows (4 per SM at most: every block leaves partial column sums behind).
+    g.gx = static_cast<int>(std::max<long long>(1, std::min<long long>(blocks, std::max(1, (backward ? 148 * blocks_fit(g) : kForwardBlocks) / groups))));
     return g;
 }
 
-template <int MODE, class TX, class TS, int VEC, int K>
+template <int MODE, class TX, class TS, class TY, int VEC, int K>
 int launch_one(bool backward, const NormParams& p, const Geometry& g, cudaStream_t s) {
     const dim3 grid(g.gx, p.width / p.group), block(g.tpu * g.upb);
     if (!backward) {
-        norm_kernel<MODE, TX, TS, VEC, K><<<grid, block, 0, s>>>(p);
-    } else {
-        const size_t smem = static_cast<size_t>(K) * block.x * VEC * sizeof(float) * (MODE == kResidual && p.part_s ? 2 : 1);
-        auto* f = norm_backward_kernel<MODE, TX, TS, VEC, K>;
-        if (smem > 40 * 1024) {
-            const int err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (err) return err;
-        }
-        f<<<grid, block, smem, s>>>(p);
+        norm_kernel<MODE, TX, TS, TY, VEC, K><<<grid, block, 0, s>>>(p);
+        return cudaGetLastError();
     }
+    const size_t smem = static_cast<size_t>(K) * block.x * VEC * sizeof(float) *
+                        (1 + (p.part_s != nullptr) + (kKeepCols<VEC, K> ? 1 + (MODE == kResidual && p.scale) : 0));
+    auto* f = norm_backward_kernel<MODE, TX, TS, TY, VEC, K>;
+    if (smem > 40 * 1024) {
+        const int err = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (err) return err;
+    }
+    f<<<grid, block, smem, s>>>(p);
     return cudaGetLastError();
 }
 
-template <int MODE, class TX, class TS>
+template <int MODE, class TX, class TS, class TY>
 int launch_vec(bool backward, const NormParams& p, const Geometry& g, cudaStream_t s) {
-    if (g.vec == 8) return g.k == 2 ? launch_one<MODE, TX, TS, 8, 2>(backward, p, g, s) : launch_one<MODE, TX, TS, 8, 4>(backward, p, g, s);
-    return g.k == 16 ? launch_one<MODE, TX, TS, 1, 16>(backward, p, g, s) : launch_one<MODE, TX, TS, 1, 32>(backward, p, g, s);
+    if (g.vec == 8)
+        return g.k == 2 ? launch_one<MODE, TX, TS, TY, 8, 2>(backward, p, g, s) : launch_one<MODE, TX, TS, TY, 8, 4>(backward, p, g, s);
+    return g.k == 16 ? launch_one<MODE, TX, TS, TY, 1, 16>(backward, p, g, s) : launch_one<MODE, TX, TS, TY, 1, 32>(backward, p, g, s);
+}
+
+template <int MODE, class TX, class TS>
+int launch_y(bool backward, const rsq_norm_config& c, const NormParams& p, const Geometry& g, cudaStream_t s) {
+    return c.y_dtype == RSQ_F32 ? launch_vec<MODE, TX, TS, float>(backward, p, g, s)
+                                : launch_vec<MODE, TX, TS, __nv_bfloat16>(backward, p, g, s);
 }
 
 template <int MODE>
 int launch_types(bool backward, const rsq_norm_config& c, const NormParams& p, const Geometry& g, cudaStream_t s) {
+    using B = __nv_bfloat16;
     if (c.x_dtype == RSQ_F32)
-        return c.side_dtype == RSQ_F32 ? launch_vec<MODE, float, float>(backward, p, g, s)
-                                       : launch_vec<MODE, float, __nv_bfloat16>(backward, p, g, s);
-    return c.side_dtype == RSQ_F32 ? launch_vec<MODE, __nv_bfloat16, float>(backward, p, g, s)
-                                   : launch_vec<MODE, __nv_bfloat16, __nv_bfloat16>(backward, p, g, s);
+        return c.side_dtype == RSQ_F32 ? launch_y<MODE, float, float>(backward, c, p, g, s) : launch_y<MODE, float, B>(backward, c, p, g, s);
+    return c.side_dtype == RSQ_F32 ? launch_y<MODE, B, float>(backward, c, p, g, s) : launch_y<MODE, B, B>(backward, c, p, g, s);
 }
 
 int launch(int mode, bool backward, const rsq_norm_config& c, const NormParams& p, const Geometry& g, cudaStream_t s) {
     switch (mode) {
-        case kPlain: return c.x_dtype == RSQ_F32 ? launch_vec<kPlain, float, float>(backward, p, g, s)
-                                                 : launch_vec<kPlain, __nv_bfloat16, float>(backward, p, g, s);
+        case kPlain: return c.x_dtype == RSQ_F32 ? launch_y<kPlain, float, float>(backward, c, p, g, s)
+                                                 : launch_y<kPlain, __nv_bfloat16, float>(backward, c, p, g, s);
         case kNormGate: return launch_types<kNormGate>(backward, c, p, g, s);
         case kGateNorm: return launch_types<kGateNorm>(backward, c, p, g, s);
         default: return launch_types<kResidual>(backward, c, p, g, s);
@@ -534,20 +572,19 @@ NormParams params(const rsq_norm_config& c, const Geometry& g) {
     p.tpu = g.tpu;
     p.upb = g.upb;
     p.eps = c.eps;
-    p.y_f32 = c.y_dtype == RSQ_F32;
     p.xs = c.x_stride;
     p.ss = c.side_stride;
     return p;
 }
 
 size_t workspace_bytes_of(const rsq_norm_config& c) {
-    return 2 * sizeof(float) * static_cast<size_t>(geometry(c).gx) * static_cast<size_t>((c.width + 3) / 4 * 4);
+    return 2 * sizeof(float) * static_cast<size_t>(geometry(c, true).gx) * static_cast<size_t>((c.width + 3) / 4 * 4);
 }
 
 // Launches a backward pass and the sums of its partial column sums.
 rsq_status run_backward(const char* who, int mode, const rsq_norm_config& c, NormParams p, float* dw, float* dscale,
                         void* workspace, size_t bytes, void* stream) {
-    const Geometry g = geometry(c);
+    const Geometry g = geometry(c, true);
     auto s = static_cast<cudaStream_t>(stream);
     if (dw || dscale) {
         if (!workspace || misaligned(workspace)) return set_error(RSQ_E_INVAL, "%s: workspace null or not 16-byte aligned", who);
@@ -557,10 +594,8 @@ rsq_status run_backward(const char* who, int mode, const rsq_norm_config& c, Nor
         p.part_s = dscale ? static_cast<float*>(workspace) + static_cast<size_t>(g.gx) * ((c.width + 3) / 4 * 4) : nullptr;
     }
     int err = launch(mode, true, c, p, g, s);
-    for (int i = 0; i < 2 && !err; ++i) {
-        float* out = i ? dscale : dw;
-        if (!out) continue;
-        column_sum_kernel<<<(c.width + 31) / 32, 256, 0, s>>>(i ? p.part_s : p.part_w, g.gx, c.width, out);
+    if (!err && (dw || dscale)) {
+        column_sum_kernel<<<dim3((c.width + 31) / 32, dscale ? 2 : 1), 1024, 0, s>>>(p.part_w, p.part_s, g.gx, c.width, dw, dscale);
         err = cudaGetLastError();
     }
     return err ? set_error(RSQ_E_CUDA, "%s: %s", who, cudaGetErrorString(static_cast<cudaError_t>(err))) : RSQ_OK;
@@ -591,7 +626,7 @@ rsq_status rsq_gated_norm(const rsq_norm_config* cfg, const void* x, const void*
     if (!x || !y) return set_error(RSQ_E_INVAL, "gated_norm: null x or y");
     for (const void* q : {x, z, static_cast<const void*>(y)})
         if (misaligned(q)) return set_error(RSQ_E_INVAL, "gated_norm: a buffer is not 16-byte aligned");
-    const Geometry g = geometry(c);
+    const Geometry g = geometry(c, false);
     NormParams p = params(c, g);
     p.x = x;
     p.side = z;
@@ -613,7 +648,7 @@ rsq_status rsq_gated_norm_backward(const rsq_norm_config* cfg, const void* x, co
     if (dz && !z) return set_error(RSQ_E_INVAL, "gated_norm_backward: dz without z");
     for (const void* q : {x, z, dy, static_cast<const void*>(dx), static_cast<const void*>(dz), static_cast<const void*>(dw)})
         if (misaligned(q)) return set_error(RSQ_E_INVAL, "gated_norm_backward: a buffer is not 16-byte aligned");
-    NormParams p = params(c, geometry(c));
+    NormParams p = params(c, geometry(c, true));
     p.x = x;
     p.side = z;
     p.w = w;
@@ -637,7 +672,7 @@ rsq_status rsq_residual_norm(const rsq_norm_config* cfg, const void* x, const vo
         if (misaligned(q)) return set_error(RSQ_E_INVAL, "residual_norm: a buffer is not 16-byte aligned");
     if (residual == h && c.side_stride != c.width)
         return set_error(RSQ_E_INVAL, "residual_norm: h is packed: in place needs a packed residual");
-    const Geometry g = geometry(c);
+    const Geometry g = geometry(c, false);
     NormParams p = params(c, g);
     p.x = x;
     p.side = residual;
@@ -663,7 +698,7 @@ rsq_status rsq_residual_norm_backward(const rsq_norm_config* cfg, const void* x,
                           static_cast<const void*>(dscale), static_cast<const void*>(dw)})
         if (misaligned(q)) return set_error(RSQ_E_INVAL, "residual_norm_backward: a buffer is not 16-byte aligned");
     c.side_stride = c.width;  // h as the forward pass wrote it
-    NormParams p = params(c, geometry(c));
+    NormParams p = params(c, geometry(c, true));
     p.x = x;
     p.side = h;
     p.scale = scale;
