@@ -53,6 +53,7 @@ struct Params {
     float* state_out;
     bf16* out;
     // workspace
+    unsigned* flag;               // kFlagTimeout when a bounded wait ran out
     float2* gb;                   // [slots][H][kChunk] b_i in two floats
     float* gdt;                   // [slots][H][kChunk] dt
     bf16* sh;                     // forward: states before the chunks [slots][H][tiles][N][kTile]
@@ -259,11 +260,27 @@ __device__ __forceinline__ void store_rows(bf16* dst, long long stride, int row0
     }
 }
 
+// One direction of the state recurrence.
+struct Pass {
+    const bf16* k;          // key rows: Bm | Cm
+    const bf16* v;          // value rows: x | dout
+    long long ks, vs;
+    const float* init;      // [n][H][N][P] or null
+    float* end;             // [n][H][N][P] or null
+    int rev;
+    int local;              // from zero to the segment's end only
+};
+
+// Whether the tcgen05 form of the state recurrence takes a shape: whole tiles of 64
+// state rows, and blocks of 128 value columns that share their keys.
+inline bool states_tc_ok(const Params& p) { return p.N >= 64 && p.P >= 64 && p.per * p.P % 128 == 0; }
+
 // Launchers (scan_forward.cu, scan_backward.cu).  Return a cudaError_t value.
 int launch_gates(const Params& p, cudaStream_t s);
 int launch_states(const Params& p, bool backward, cudaStream_t s);  // with the segments' two passes, if any
 int launch_out(const Params& p, int head_set, cudaStream_t s);
 int launch_step(const Params& p, cudaStream_t s);
+int launch_states_tc(const Params& p, bool backward, const Pass& f, const Pass& b, cudaStream_t s);  // one launch
 int launch_backward(const Params& p, int head_set, cudaStream_t s);
 
 }  // namespace scan

@@ -77,6 +77,7 @@ size_t layout(const rsq_scan_config& c, bool backward, Params* p, uint8_t* base)
     };
     const size_t cells = static_cast<size_t>(p->slots) * p->H;
     const size_t state = static_cast<size_t>(p->N) * kTile * p->tiles;
+    p->flag = reinterpret_cast<unsigned*>(take(sizeof(unsigned)));
     p->gb = reinterpret_cast<float2*>(take(cells * kChunk * sizeof(float2)));
     p->gdt = reinterpret_cast<float*>(take(cells * kChunk * sizeof(float)));
     if (backward) {

@@ -15,6 +15,7 @@ namespace {
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads) gates_kernel(const __grid_constant__ Params p) {
     const int slot = blockIdx.x, lane = threadIdx.x & 31;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.flag = 0u;
     const int h = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5);
     const Range r = slot_range(p, slot, kChunk);
     if (h >= p.H || !r.valid) return;
@@ -68,16 +69,6 @@ __global__ void __launch_bounds__(kThreads) gates_kernel(const __grid_constant__
 // The backward recurrence is the same with (C, dout, 2^b_i) for (B, x, weights)
 // and the chunks in reverse.
 // ---------------------------------------------------------------------------
-struct Pass {
-    const bf16* k;          // key rows: Bm | Cm
-    const bf16* v;          // value rows: x | dout
-    long long ks, vs;
-    const float* init;      // [n][H][N][P] or null
-    float* end;             // [n][H][N][P] or null
-    int rev;
-    int local;              // from zero to the segment's end only
-};
-
 template <int N>
 struct StateShape {
     static constexpr int kRows = N >= 128 ? N / 128 : 1;    // 16-row blocks of a warp
@@ -560,19 +551,23 @@ int allow_smem(F* f, int bytes) {
 template <int N>
 int states_n(const Params& p, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
     using Sh = StateShape<N>;
+    if (N >= 64 && states_tc_ok(p)) return launch_states_tc(p, backward, f, b, s);
     const dim3 grid(p.seg_chunks ? p.seg_slots : p.n, p.H * p.tiles, backward ? 2 : 1);
     auto* k = backward ? states_kernel<N, true> : states_kernel<N, false>;
-    int err = allow_smem(k, Sh::kSmem);
-    if (!err && p.seg_chunks) {
-        Pass lf = f, lb = b;
-        lf.local = lb.local = 1;
-        k<<<grid, kThreads, Sh::kSmem, s>>>(p, lf, lb);
-        segments_kernel<<<dim3((N * p.P / 4 + kThreads - 1) / kThreads, p.H, 2 * p.n), kThreads, 0, s>>>(p, f, b);
-        err = cudaGetLastError();
-    }
+    const int err = allow_smem(k, Sh::kSmem);
     if (err) return err;
     k<<<grid, kThreads, Sh::kSmem, s>>>(p, f, b);
     return cudaGetLastError();
+}
+
+int states_pass(const Params& p, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
+    switch (p.N) {
+        case 16: return states_n<16>(p, backward, f, b, s);
+        case 32: return states_n<32>(p, backward, f, b, s);
+        case 64: return states_n<64>(p, backward, f, b, s);
+        case 128: return states_n<128>(p, backward, f, b, s);
+        default: return states_n<256>(p, backward, f, b, s);
+    }
 }
 
 template <int N>
@@ -595,13 +590,15 @@ int launch_gates(const Params& p, cudaStream_t s) {
 int launch_states(const Params& p, bool backward, cudaStream_t s) {
     const Pass f{p.Bm, p.x, p.bs, p.xs, p.state_in, p.state_out, 0, 0};
     const Pass b{backward ? p.Cm : nullptr, p.dout, p.cs, static_cast<long long>(p.H) * p.P, p.dstate_out, p.dstate_in, 1, 0};
-    switch (p.N) {
-        case 16: return states_n<16>(p, backward, f, b, s);
-        case 32: return states_n<32>(p, backward, f, b, s);
-        case 64: return states_n<64>(p, backward, f, b, s);
-        case 128: return states_n<128>(p, backward, f, b, s);
-        default: return states_n<256>(p, backward, f, b, s);
+    if (p.seg_chunks) {
+        Pass lf = f, lb = b;
+        lf.local = lb.local = 1;
+        int err = states_pass(p, backward, lf, lb, s);
+        if (err) return err;
+        segments_kernel<<<dim3((p.N * p.P / 4 + kThreads - 1) / kThreads, p.H, 2 * p.n), kThreads, 0, s>>>(p, f, b);
+        if ((err = cudaGetLastError())) return err;
     }
+    return states_pass(p, backward, f, b, s);
 }
 
 int launch_step(const Params& p, cudaStream_t s) {
