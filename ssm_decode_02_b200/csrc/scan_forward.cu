@@ -614,6 +614,7 @@ int launch_step(const Params& p, cudaStream_t s) {
 }
 
 int launch_out(const Params& p, int head_set, cudaStream_t s) {
+    if (out_tc_ok(p)) return launch_out_tc(p, head_set, s);
     switch (p.N) {
         case 16: return out_n<16>(p, head_set, s);
         case 32: return out_n<32>(p, head_set, s);

@@ -1,0 +1,316 @@
+// scan_out_tc.cu -- the scan's outputs on the fifth-generation tensor cores
+// (tcgen05): the form of out_kernel (scan_forward.cu) for dk of 64 and 128 and heads
+// of whole 64-column tiles.
+//
+// A block takes one chunk and some heads of one group.  The scores C_i.B_j, which do
+// not depend on the head, are one product whose 128 x 128 result stays in the
+// registers of the scorers; per tile of 64 columns of a head
+//     inter = C S_0 (keys' rows from shared memory)       128 x 64, k = N
+//     intra = (scores . decays . dt) x                    128 x 64, k = tokens
+//     out   = 2^b_i inter + intra + D x
+// with the left operand of `intra` in tensor memory, where the scorers write it.
+// Warps, which meet at mbarriers only:
+//   16 scorers    a warp 32 rows by 32 columns of the scores; per head they make the
+//                 decays and write the bf16 left operand (two buffers);
+//   2 x 4 writers every other tile: a thread one row of 64 columns; the output goes
+//                 over x in shared memory and from there to memory in whole lines;
+//   2 loaders     x and the state of each tile, four stages;
+//   1 issuer      of the products.
+// The decay between a row and a column is the product of two powers that meet at the
+// border between their blocks of 32 tokens (at most 1 each where decays are): two
+// powers per lane and head in the place of 32.  On the diagonal they meet at the
+// block's start and one of them grows with the decay over it, so that a block which
+// decays by more than 2^60 takes a power per pair.
+#include "tc.cuh"
+
+namespace rsq {
+namespace scan {
+namespace {
+
+constexpr int kStages = 4;
+constexpr int kScorers = 512, kWriters = 256, kLoaders = 64;
+constexpr int kBlock = kScorers + kWriters + kLoaders + 32;
+constexpr int kTmem = 512;                                  // scores, 2 x (inter, intra), 2 x left operand
+constexpr int kD = 128, kLeft = 384;
+
+template <int N>
+struct Shape {
+    static constexpr int kKeys = kChunk * N * 2;
+    static constexpr int kX = kChunk * kTile * 2;
+    static constexpr int kStage = kX + N * kTile * 2;
+    static constexpr int kGates = 16 * 32 * (4 + 16);       // per scorer warp: factors; b in two floats, dt
+    static constexpr int kSmem = 1024 + 2 * kKeys + kStages * kStage + kGates + 256;
+};
+
+template <int N>
+__global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant__ Params p, int head_set) {
+    using Sh = Shape<N>;
+    extern __shared__ uint8_t raw_smem[];
+    const Range rg = slot_range(p, blockIdx.x, kChunk);
+    if (!rg.valid) return;
+    const int sets = (p.per + head_set - 1) / head_set;
+    const int group = blockIdx.y / sets, set = blockIdx.y - group * sets;
+    const int h0 = group * p.per + set * head_set;
+    const int items = min(head_set, p.per - set * head_set) * p.tiles;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int valid = rg.valid;
+
+    uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
+    const uint32_t sc = smem_u32(smem), sb = sc + Sh::kKeys, stages = sb + Sh::kKeys;
+    uint8_t* gates = smem + 2 * Sh::kKeys + kStages * Sh::kStage;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gates + Sh::kGates);
+    // barriers: keys loaded; scores done; stage loaded x4; stage free x4; left operand
+    // written x2; free x2; tile done x2; free x2
+    const uint32_t keys = smem_u32(tmem_slot + 2), scores = keys + 8, loaded = scores + 8, emptied = loaded + 32, left = emptied + 32,
+                   left_free = left + 16, tile_done = left_free + 16, tile_free = tile_done + 16;
+    if (warp == 0) tc::tmem_alloc(smem_u32(tmem_slot), kTmem);
+    if (threadIdx.x == 0) {
+        mbar_init(keys, kLoaders);
+        mbar_init(scores, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(loaded + 8 * i, kLoaders);
+            mbar_init(emptied + 8 * i, 128);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(left + 8 * i, kScorers);
+            mbar_init(left_free + 8 * i, 1);
+            mbar_init(tile_done + 8 * i, 1);
+            mbar_init(tile_free + 8 * i, 128);
+        }
+        fence_mbar_init();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t lanes = (static_cast<uint32_t>(warp) & 3) << 21;
+
+    if (threadIdx.x < kScorers) {
+        const int quarter = warp & 3, cols = warp >> 2, row = quarter * 32 + lane;   // rows 32 quarter .., columns 32 cols ..
+        float g[32];
+        bool ok = tc::wait_warp(scores, 0, p.flag);
+        if (ok) {
+            tc::fence_after();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float v[16];
+                tc::tmem_ld16(v, tmem + cols * 32 + i * 16 + lanes);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) g[i * 16 + k] = v[k];
+            }
+        }
+        float* fac = reinterpret_cast<float*>(gates) + warp * 32;
+        float4* pair = reinterpret_cast<float4*>(gates + 16 * 32 * 4) + warp * 32;
+        const int heads = items / p.tiles;
+        const bool diagonal = cols == quarter;
+        const long long at0 = (static_cast<long long>(blockIdx.x) * p.H + h0) * kChunk;
+        float2 nc = make_float2(0.f, 0.f), nr = nc;
+        float nd = 0.f;
+        auto read = [&](int i) {
+            if (i >= heads || cols > quarter) return;
+            const long long at = at0 + static_cast<long long>(i) * kChunk;
+            nc = p.gb[at + cols * 32 + lane];
+            nd = p.gdt[at + cols * 32 + lane];
+            nr = p.gb[at + row];
+        };
+        read(0);
+        for (int i = 0; i < heads && ok; ++i) {
+            const int buf = i & 1;
+            const float2 bc = nc, br = nr;
+            const float dt = nd;
+            read(i + 1);
+            if (i >= 2 && !(ok = tc::wait_warp(left_free + 8 * buf, i / 2 - 1, p.flag))) break;
+            tc::fence_after();
+            const uint32_t dst = tmem + kLeft + buf * 64 + cols * 16 + lanes;
+            if (cols > quarter) {           // behind every row: zero, once for each buffer
+                if (i < 2) {
+                    const uint32_t z[16] = {};
+                    tc::tmem_st16(dst, z);
+                }
+            } else {
+                const int meet = diagonal ? 0 : 31;
+                const float2 bm = make_float2(__shfl_sync(0xffffffffu, bc.x, meet), __shfl_sync(0xffffffffu, bc.y, meet));
+                const float last = __shfl_sync(0xffffffffu, bc.x, 31);
+                __syncwarp();
+                fac[lane] = dt * ex2_diff(bm, bc);
+                const float r = ex2_diff(br, bm);
+                const bool direct = diagonal && !(bm.x - last < 60.f);
+                if (direct) pair[lane] = make_float4(bc.x, bc.y, dt, 0.f);
+                __syncwarp();
+                uint32_t w[16];
+                if (!direct) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 f = reinterpret_cast<const float4*>(fac)[k];
+                        float v[4] = {g[4 * k] * (r * f.x), g[4 * k + 1] * (r * f.y), g[4 * k + 2] * (r * f.z), g[4 * k + 3] * (r * f.w)};
+                        if (diagonal) {
+#pragma unroll
+                            for (int o = 0; o < 4; ++o) v[o] = 4 * k + o <= lane ? v[o] : 0.f;
+                        }
+                        w[2 * k] = pack(v[0], v[1]);
+                        w[2 * k + 1] = pack(v[2], v[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float v[2];
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            const float4 q = pair[2 * k + o];
+                            v[o] = 2 * k + o <= lane ? g[2 * k + o] * (ex2_diff(br, make_float2(q.x, q.y)) * q.z) : 0.f;
+                        }
+                        w[k] = pack(v[0], v[1]);
+                    }
+                }
+                tc::tmem_st16(dst, w);
+            }
+            tc::tmem_st_wait();
+            tc::fence_before();
+            mbar_arrive(left + 8 * buf);
+        }
+    } else if (threadIdx.x < kScorers + kWriters) {
+        const int ww = warp - kScorers / 32, wg = ww >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const long long os = static_cast<long long>(p.H) * p.P;
+        float2 nb = make_float2(0.f, 0.f);
+        float nd = 0.f;
+        auto read = [&](int it) {
+            if (it >= items) return;
+            const int h = h0 + it / p.tiles;
+            nb = p.gb[(static_cast<long long>(blockIdx.x) * p.H + h) * kChunk + row];
+            if (p.D) nd = __ldg(p.D + h);
+        };
+        read(wg);
+        for (int it = wg; it < items; it += 2) {
+            const int h = h0 + it / p.tiles, tile = it % p.tiles;
+            const float d = nd, e = ex2(nb.x + nb.y);
+            read(it + 2);
+            const uint32_t st = stages + (it % kStages) * Sh::kStage;
+            if (!tc::wait_warp(tile_done + 8 * wg, it / 2, p.flag)) break;
+            tc::fence_after();
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                float a[16], v[16];
+                tc::tmem_ld16(a, tmem + kD + wg * 128 + s * 16 + lanes);
+                tc::tmem_ld16(v, tmem + kD + wg * 128 + 64 + s * 16 + lanes);
+                tc::tmem_ld_wait();
+                if (s == 3) {
+                    tc::fence_before();
+                    mbar_arrive(tile_free + 8 * wg);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t ad = st + tile_at<128>(row, s * 2 + k);
+                    uint32_t x[4], o[4];
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(ad) : "memory");
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = k * 8 + 2 * i;
+                        o[i] = pack(fmaf(d, lo_of(x[i]), fmaf(e, a[c], v[c])), fmaf(d, hi_of(x[i]), fmaf(e, a[c + 1], v[c + 1])));
+                    }
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ad), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+                }
+            }
+            __syncwarp();
+            // this warp's 32 rows, four whole rows at a time
+            bf16* out = p.out + static_cast<long long>(rg.first) * os + static_cast<long long>(h) * p.P + tile * kTile;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = quarter * 32 + k * 4 + (lane >> 3);
+                uint4 v;
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                             : "r"(st + tile_at<128>(r, lane & 7)) : "memory");
+                if (r < valid) *reinterpret_cast<uint4*>(out + r * os + (lane & 7) * 8) = v;
+            }
+            mbar_arrive(emptied + 8 * (it % kStages));
+        }
+    } else if (threadIdx.x < kScorers + kWriters + kLoaders) {
+        const int i0 = threadIdx.x - kScorers - kWriters, t = i0 >> 3, c = i0 & 7;   // rows t + 8 j, columns 8 c ..
+        const uint32_t place = tile_at<128>(t, c);
+        auto rows = [&](uint32_t dst, const bf16* src, long long stride, int n, int on_rows) {
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) {
+                const bool on = t + 8 * j < on_rows;
+                cp16(dst + place + j * 1024, src + (on ? (t + 8 * j) * stride : 0) + c * 8, on);
+            }
+        };
+#pragma unroll
+        for (int b = 0; b < N / 64; ++b) {
+            rows(sc + b * kChunk * 128, p.Cm + rg.first * p.cs + group * N + b * 64, p.cs, kChunk / 8, valid);
+            rows(sb + b * kChunk * 128, p.Bm + rg.first * p.bs + group * N + b * 64, p.bs, kChunk / 8, valid);
+        }
+        cp_commit();
+        // two stages are on their way while the one before them is waited for
+        for (int it = 0; it <= items + 1; ++it) {
+            if (it < items) {
+                const int h = h0 + it / p.tiles, tile = it % p.tiles;
+                const uint32_t st = stages + (it % kStages) * Sh::kStage;
+                if (it >= kStages && !tc::wait_warp(emptied + 8 * (it % kStages), it / kStages - 1, p.flag)) break;
+                rows(st, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs, kChunk / 8, valid);
+                const long long cell = (static_cast<long long>(blockIdx.x) * p.H + h) * p.tiles + tile;
+                rows(st + Sh::kX, p.sh + cell * N * kTile, kTile, N / 8, N);
+            }
+            cp_commit();
+            if (it == 1) continue;
+            if (it == 0)
+                cp_wait<1>();
+            else
+                cp_wait<2>();
+            tc::fence_smem();
+            mbar_arrive(it == 0 ? keys : loaded + 8 * ((it - 2) % kStages));
+        }
+        cp_wait<0>();
+    } else if (lane == 0) {
+        bool ok = mbar_wait(keys, 0, kWaitIters);
+        if (ok) {
+            constexpr uint32_t id = tc::idesc(kChunk, false, false);
+#pragma unroll
+            for (int ks = 0; ks < N / 16; ++ks) {
+                const uint32_t o = (ks / 4) * kChunk * 128 + (ks % 4) * 32;
+                tc::mma(tmem, tc::desc(sc + o, 16), tc::desc(sb + o, 16), id, ks);
+            }
+            tc::commit(scores);
+        }
+        constexpr uint32_t id = tc::idesc(kTile, false, true);
+        for (int it = 0; it < items && ok; ++it) {
+            const int head = it / p.tiles, tile = it % p.tiles, buf = head & 1;
+            const uint32_t st = stages + (it % kStages) * Sh::kStage, d = tmem + kD + (it & 1) * 128;
+            if (!(ok = mbar_wait(loaded + 8 * (it % kStages), (it / kStages) & 1, kWaitIters))) break;
+            if (it >= 2 && !(ok = mbar_wait(tile_free + 8 * (it & 1), (it / 2 - 1) & 1, kWaitIters))) break;
+            tc::fence_after();
+#pragma unroll
+            for (int ks = 0; ks < N / 16; ++ks)
+                tc::mma(d, tc::desc(sc + (ks / 4) * kChunk * 128 + (ks % 4) * 32, 16), tc::desc(st + Sh::kX + ks * 2048, 16), id, ks);
+            if (tile == 0) {
+                if (!(ok = mbar_wait(left + 8 * buf, (head / 2) & 1, kWaitIters))) break;
+                tc::fence_after();
+            }
+#pragma unroll
+            for (int ks = 0; ks < kChunk / 16; ++ks) tc::mma_ta(d + 64, tmem + kLeft + buf * 64 + ks * 8, tc::desc(st + ks * 2048, 16), id, ks);
+            tc::commit(tile_done + 8 * (it & 1));
+            if (tile == p.tiles - 1) tc::commit(left_free + 8 * buf);
+        }
+        if (!ok) atomicOr(p.flag, kFlagTimeout);
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) tc::tmem_free(tmem, kTmem);
+}
+
+template <int N>
+int run(const Params& p, int head_set, cudaStream_t s) {
+    const int err = cudaFuncSetAttribute(out_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<N>::kSmem);
+    if (err) return err;
+    const dim3 grid(p.slots, p.G * ((p.per + head_set - 1) / head_set));
+    out_tc_kernel<N><<<grid, kBlock, Shape<N>::kSmem, s>>>(p, head_set);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int launch_out_tc(const Params& p, int head_set, cudaStream_t s) {
+    return p.N == 64 ? run<64>(p, head_set, s) : run<128>(p, head_set, s);
+}
+
+}  // namespace scan
+}  // namespace rsq

@@ -84,12 +84,6 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
     tc::fence_after();
     const uint32_t tmem = *tmem_slot;
     auto chunk_of = [&](int s) { return ps.rev ? chunks - 1 - s / 2 : s / 2; };
-    auto wait = [&](uint32_t bar, int phase) {
-        if (mbar_wait(bar, phase & 1, kWaitIters)) return true;
-        atomicOr(p.flag, kFlagTimeout);
-        return false;
-    };
-
     if (threadIdx.x < kConverters) {
         // this thread's chunks: rows t and t + 32, columns 8 c.. of every 64 x 64 tile
         const int t = threadIdx.x >> 3, c = threadIdx.x & 7;
@@ -142,7 +136,7 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
             read_gates(s + 1);
             cp_wait<1>();
             // the products of step s - 2 are done with the terms' buffer and with the stage loaded below
-            if (s >= 2 && !wait(done + 8 * (s & 1), s / 2 - 1)) break;
+            if (s >= 2 && !tc::wait_warp(done + 8 * (s & 1), s / 2 - 1, p.flag)) break;
             const uint32_t st = base + (s % kStages) * Sh::kStage + Sh::kKeys + place, tb = terms + (s & 1) * Sh::kTerms + place;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
@@ -197,7 +191,7 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
                 }
             }
             const float a = ex2(end.x + end.y);
-            if (!(ok = wait(full + 8 * (i & 1), i / 2))) break;
+            if (!(ok = tc::wait_warp(full + 8 * (i & 1), i / 2, p.flag))) break;
             tc::fence_after();
             const uint32_t d = tmem + (i & 1) * N + n0 + ((static_cast<uint32_t>(warp) & 3) << 21);
 #pragma unroll
@@ -227,8 +221,12 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
     } else if (lane == 0) {
         constexpr uint32_t id = tc::idesc(N, true, true);
         for (int s = 0; s < steps; ++s) {
-            if (!wait(written + 8 * (s & 1), s / 2)) break;
-            if (!(s & 1) && s >= 4 && !wait(taken + 8 * ((s / 2) & 1), s / 4 - 1)) break;
+            bool ok = mbar_wait(written + 8 * (s & 1), (s / 2) & 1, kWaitIters);
+            if (ok && !(s & 1) && s >= 4) ok = mbar_wait(taken + 8 * ((s / 2) & 1), (s / 4 - 1) & 1, kWaitIters);
+            if (!ok) {
+                atomicOr(p.flag, kFlagTimeout);
+                break;
+            }
             tc::fence_after();
             const uint32_t st = base + (s % kStages) * Sh::kStage, tb = terms + (s & 1) * Sh::kTerms;
             const uint32_t d = tmem + ((s / 2) & 1) * N;

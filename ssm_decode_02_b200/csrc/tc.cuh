@@ -89,12 +89,12 @@ __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// A bounded wait that the whole block takes part in: false (for every thread) when
-// it ran out, with the call's flag set.  Also a barrier.
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, unsigned* flag) {
-    const bool ok = mbar_wait(bar, parity, kWaitIters);
-    if (!ok && threadIdx.x == 0) atomicOr(flag, kFlagTimeout);
-    return __syncthreads_and(ok);
+// A bounded wait of one warp, the same answer for every lane: false when it ran out,
+// with the call's flag set.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, int phase, unsigned* flag) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, kWaitIters));
+    if (!ok && (threadIdx.x & 31) == 0) atomicOr(flag, kFlagTimeout);
+    return ok;
 }
 
 }  // namespace tc
