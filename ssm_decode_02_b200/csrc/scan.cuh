@@ -278,6 +278,9 @@ inline bool states_tc_ok(const Params& p) { return p.N >= 64 && p.P >= 64 && p.p
 // The same for the outputs.
 inline bool out_tc_ok(const Params& p) { return (p.N == 64 || p.N == 128) && p.P >= 64; }
 
+// The same for dx and the gates' gradients (two stages hold a head's tiles).
+inline bool dx_tc_ok(const Params& p) { return (p.N == 64 || p.N == 128) && (p.P == 64 || p.P == 128); }
+
 // Launchers (scan_forward.cu, scan_backward.cu).  Return a cudaError_t value.
 int launch_gates(const Params& p, cudaStream_t s);
 int launch_states(const Params& p, bool backward, cudaStream_t s);  // with the segments' two passes, if any
@@ -285,6 +288,7 @@ int launch_out(const Params& p, int head_set, cudaStream_t s);
 int launch_out_tc(const Params& p, int head_set, cudaStream_t s);
 int launch_step(const Params& p, cudaStream_t s);
 int launch_states_tc(const Params& p, bool backward, const Pass& f, const Pass& b, cudaStream_t s);  // one launch
+int launch_dx_tc(const Params& p, int head_set, cudaStream_t s);
 int launch_backward(const Params& p, int head_set, cudaStream_t s);
 
 }  // namespace scan

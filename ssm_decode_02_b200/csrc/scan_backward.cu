@@ -575,8 +575,12 @@ int backward_n(const Params& p, int head_set, cudaStream_t s) {
     if (err) return err;
     if (p.slots) {
         const dim3 grid(p.slots, p.G * ((p.per + head_set - 1) / head_set));
-        dx_kernel<N><<<grid, kThreads, DxShape<N>::kSmem, s>>>(p, head_set);
-        err = cudaGetLastError();
+        if (dx_tc_ok(p)) {
+            err = launch_dx_tc(p, head_set, s);
+        } else {
+            dx_kernel<N><<<grid, kThreads, DxShape<N>::kSmem, s>>>(p, head_set);
+            err = cudaGetLastError();
+        }
         if (!err && (p.dBm || p.dCm)) {
             dk_kernel<N><<<dim3(p.slots, p.G * (N / DkShape<N>::kW), 2), kThreads, DkShape<N>::kSmem, s>>>(p);
             err = cudaGetLastError();

@@ -1,0 +1,545 @@
+// scan_dx_tc.cu -- dx and the gates' gradients on the fifth-generation tensor cores
+// (tcgen05): the form of dx_kernel (scan_backward.cu, which has the formulas) for dk
+// and dv of 64 and 128.
+//
+// A block takes one chunk and some heads of one group.  In tensor memory lie
+//     g  = B C^T     128 x 128 tokens (j, i), once
+//     w  = x dout^T  128 x 128 per head
+//     pt = g . decays (bf16, left operand), i >= j
+//     c  = pt dout   128 x 64 per tile of 64 columns
+//     d  = B dS,  e = C S_0   128 x 64 per tile, the state in three bf16 terms
+// with dx = dt (c + 2^(b_end-b_j) d) + D dout; the gates' sums are those of w . pt by
+// row and by column (before pt is rounded), and the rows' products of d with x and of
+// e with dout.  Warps, which meet at mbarriers only:
+//   8 scorers     pt, and the sums of w . pt (by column: a transposing reduction over the lanes)
+//   4 + 4 writers dx with its row sums; the row sums of e
+//   8 converters  the states, binary32 in memory, to three terms; <S_0, dS>
+//   2 loaders     x and dout, two stages
+//   1 finisher    the gates' gradients of a head from the sums
+//   1 issuer      of the products.
+#include "tc.cuh"
+
+namespace rsq {
+namespace scan {
+namespace {
+
+constexpr int kScorers = 256, kWriters = 256, kConverters = 256, kLoaders = 64;
+constexpr int kBlock = kScorers + kWriters + kConverters + kLoaders + 64;
+constexpr int kUnits = 3;                       // ring of 64 state rows in three terms
+constexpr int kPlane = 64 * kTile * 2, kUnit = 3 * kPlane;
+constexpr int kG = 0, kW = 128, kC = 256, kDd = 320, kE = 384, kPt = 448;
+// sums of one head (floats)
+constexpr int kRow = 0, kOwn = 256, kCol = 384, kIn = 896, kFin = 1024, kDot = 1152, kThrough = 1280, kSums = 1288;
+
+template <int N>
+struct Shape {
+    static constexpr int kKeys = kChunk * N * 2;
+    static constexpr int kX = kChunk * kTile * 2;
+    static constexpr int kSmem = 1024 + 2 * kKeys + 4 * kX + kUnits * kUnit + 8 * 32 * (2 * 4 + 8) + 2 * kSums * 4 + 256;
+};
+
+// v[k] of the 32 lanes added up; lane l gets the sum of v[l].
+__device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int k = 0; k < d; ++k) {
+            const float keep = up ? v[k + d] : v[k], send = up ? v[k] : v[k + d];
+            v[k] = keep + __shfl_xor_sync(0xffffffffu, send, d);
+        }
+    }
+    return v[0];
+}
+
+template <int N>
+__global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant__ Params p, int head_set) {
+    using Sh = Shape<N>;
+    extern __shared__ uint8_t raw_smem[];
+    const Range rg = slot_range(p, blockIdx.x, kChunk);
+    const int sets = (p.per + head_set - 1) / head_set;
+    const int group = blockIdx.y / sets, set = blockIdx.y - group * sets;
+    const int h0 = group * p.per + set * head_set;
+    const int heads = min(head_set, p.per - set * head_set), items = heads * p.tiles;
+    const long long cells0 = static_cast<long long>(blockIdx.x) * p.H;
+    if (!rg.valid) {
+        // no rows: this slot adds nothing to the sums over tokens
+        for (int i = threadIdx.x; i < heads; i += kBlock) {
+            p.part[cells0 + h0 + i] = 0.f;
+            p.part[static_cast<long long>(p.slots) * p.H + cells0 + h0 + i] = 0.f;
+        }
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, valid = rg.valid;
+    const long long os = static_cast<long long>(p.H) * p.P;
+
+    uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
+    const uint32_t sb = smem_u32(smem), sc = sb + Sh::kKeys, stages = sc + Sh::kKeys, units = stages + 4 * Sh::kX;
+    float* facs = reinterpret_cast<float*>(smem + 2 * Sh::kKeys + 4 * Sh::kX + kUnits * kUnit);   // [8 warps][2][32]
+    float2* pairs = reinterpret_cast<float2*>(facs + 8 * 64);                                      // [8 warps][32]
+    float* sums = reinterpret_cast<float*>(pairs + 8 * 32);                                        // [2][kSums]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums + 2 * kSums);
+    uint32_t bar = smem_u32(tmem_slot + 2);
+    auto next_bar = [&](int n) {
+        const uint32_t b = bar;
+        bar += 8 * n;
+        return b;
+    };
+    const uint32_t keys = next_bar(1), g_done = next_bar(1), loaded = next_bar(2), emptied = next_bar(2), unit_written = next_bar(kUnits),
+                   unit_free = next_bar(kUnits), w_done = next_bar(1), w_free = next_bar(1), pt_written = next_bar(1),
+                   pt_free = next_bar(1), cd_done = next_bar(1), cd_free = next_bar(1), e_done = next_bar(1), e_free = next_bar(1),
+                   sums_done = next_bar(2), sums_free = next_bar(2);
+    if (warp == 0) tc::tmem_alloc(smem_u32(tmem_slot), 512);
+    if (threadIdx.x == 0) {
+        mbar_init(keys, kLoaders);
+        for (uint32_t b : {g_done, w_done, pt_free, cd_done, e_done}) mbar_init(b, 1);
+        for (uint32_t b : {w_free, pt_written}) mbar_init(b, kScorers);
+        for (uint32_t b : {cd_free, e_free}) mbar_init(b, 128);
+        for (int i = 0; i < kUnits; ++i) {
+            mbar_init(unit_written + 8 * i, kConverters);
+            mbar_init(unit_free + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(loaded + 8 * i, kLoaders);
+            mbar_init(emptied + 8 * i, kWriters);
+            mbar_init(sums_done + 8 * i, kScorers + kWriters + kConverters);
+            mbar_init(sums_free + 8 * i, 32);
+        }
+        fence_mbar_init();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot, lanes = (static_cast<uint32_t>(warp) & 3) << 21;
+    const int quarter = warp & 3, row = quarter * 32 + lane;   // of the warps that reach tensor memory
+
+    if (threadIdx.x < kScorers) {
+        const int half = warp >> 2;                             // columns 64 half ..
+        float* fac = facs + warp * 64;
+        float2* pair = pairs + warp * 32;
+        const bool any = half * 2 + 1 >= quarter;               // some block of its columns is not before its rows
+        float2 nc[2], nr = make_float2(0.f, 0.f);
+        float nd = 0.f;
+        auto read = [&](int i) {
+            if (i >= heads || !any) return;
+            const long long at = (cells0 + h0 + i) * kChunk;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) nc[k] = p.gb[at + half * 64 + k * 32 + lane];
+            nr = p.gb[at + row];
+            nd = p.gdt[at + row];
+        };
+        read(0);
+        bool ok = tc::wait_warp(g_done, 0, p.flag);
+        for (int i = 0; i < heads && ok; ++i) {
+            float2 bc[2] = {nc[0], nc[1]};
+            const float2 br = nr;
+            const float dt = nd;
+            read(i + 1);
+            if (!(ok = tc::wait_warp(w_done, i, p.flag))) break;
+            if (i && !(ok = tc::wait_warp(pt_free, i - 1, p.flag))) break;
+            if (i >= 2 && !(ok = tc::wait_warp(sums_free + 8 * (i & 1), i / 2 - 1, p.flag))) break;
+            tc::fence_after();
+            float* out = sums + (i & 1) * kSums;
+            float rows = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int cols = half * 2 + k;                  // this block of 32 columns
+                const uint32_t dst = tmem + kPt + cols * 16 + lanes;
+                if (cols < quarter) {                           // before every row: zero, once
+                    if (i == 0) {
+                        const uint32_t z[4] = {};
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) tc::tmem_st4(dst + 4 * s, z);
+                    }
+                    continue;
+                }
+                const bool diagonal = cols == quarter;
+                const int meet = diagonal ? 31 : 0;
+                const float2 bm = make_float2(__shfl_sync(0xffffffffu, bc[k].x, meet), __shfl_sync(0xffffffffu, bc[k].y, meet));
+                const float first = __shfl_sync(0xffffffffu, bc[k].x, 0);
+                const float r = ex2_diff(bm, br);
+                const bool direct = diagonal && !(first - bm.x < 60.f);
+                __syncwarp();
+                fac[k * 32 + lane] = ex2_diff(bc[k], bm);
+                if (direct) pair[lane] = bc[k];
+                __syncwarp();
+                float v[32], own = 0.f;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    float g[8], w[8];
+                    tc::tmem_ld8(g, tmem + kG + cols * 32 + s * 8 + lanes);
+                    tc::tmem_ld8(w, tmem + kW + cols * 32 + s * 8 + lanes);
+                    tc::tmem_ld_wait();
+                    uint32_t o[4];
+                    if (!direct) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const float4 f = reinterpret_cast<const float4*>(fac + k * 32)[s * 2 + q];
+                            g[4 * q] *= r * f.x;
+                            g[4 * q + 1] *= r * f.y;
+                            g[4 * q + 2] *= r * f.z;
+                            g[4 * q + 3] *= r * f.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) g[q] *= ex2_diff(s * 8 + q >= lane ? pair[s * 8 + q] : br, br);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int c = s * 8 + q;
+                        if (diagonal && c < lane) g[q] = 0.f;
+                        w[q] *= g[q];
+                        if (diagonal && c < lane) w[q] = 0.f;
+                        if (diagonal && c == lane) {
+                            own = w[q];
+                            w[q] = 0.f;
+                        }
+                        rows += w[q];
+                        v[c] = w[q] * dt;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) o[q] = pack(g[2 * q], g[2 * q + 1]);
+                    tc::tmem_st4(dst + 4 * s, o);
+                }
+                out[kCol + quarter * 128 + cols * 32 + lane] = transpose_sum(v, lane);
+                if (diagonal) out[kOwn + row] = own;
+            }
+            out[kRow + half * 128 + row] = rows;
+            tc::tmem_st_wait();
+            tc::fence_before();
+            mbar_arrive(w_free);
+            mbar_arrive(pt_written);
+            mbar_arrive(sums_done + 8 * (i & 1));
+        }
+    } else if (threadIdx.x < kScorers + kWriters / 2) {
+        // dx
+        float fin = 0.f, dot = 0.f;
+        float2 nb = make_float2(0.f, 0.f), ne = nb;
+        float nd = 0.f, nD = 0.f;
+        auto read = [&](int it) {
+            if (it >= items) return;
+            const int h = h0 + it / p.tiles;
+            nb = p.gb[(cells0 + h) * kChunk + row];
+            ne = p.gb[(cells0 + h) * kChunk + kChunk - 1];
+            nd = p.gdt[(cells0 + h) * kChunk + row];
+            if (p.D) nD = __ldg(p.D + h);
+        };
+        read(0);
+        for (int it = 0; it < items; ++it) {
+            const int head = it / p.tiles, tile = it - head * p.tiles, h = h0 + head;
+            const float w = ex2_diff(ne, nb), dt = nd, D = nD;
+            read(it + 1);
+            const uint32_t sx = stages + (it & 1) * 2 * Sh::kX, sy = sx + Sh::kX;
+            if (!tc::wait_warp(cd_done, it, p.flag)) break;
+            tc::fence_after();
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                float c[8], d[8];
+                tc::tmem_ld8(c, tmem + kC + s * 8 + lanes);
+                tc::tmem_ld8(d, tmem + kDd + s * 8 + lanes);
+                uint32_t x[4], y[4], o[4];
+                const uint32_t ax = sx + tile_at<128>(row, s);
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(ax) : "memory");
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                             : "r"(sy + tile_at<128>(row, s)) : "memory");
+                tc::tmem_ld_wait();
+                if (s == 7) {
+                    tc::fence_before();
+                    mbar_arrive(cd_free);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float d0 = d[2 * k] * w, d1 = d[2 * k + 1] * w;
+                    fin = fmaf(d0, lo_of(x[k]), fmaf(d1, hi_of(x[k]), fin));
+                    dot = fmaf(lo_of(y[k]), lo_of(x[k]), fmaf(hi_of(y[k]), hi_of(x[k]), dot));
+                    o[k] = pack(fmaf(dt, c[2 * k] + d0, D * lo_of(y[k])), fmaf(dt, c[2 * k + 1] + d1, D * hi_of(y[k])));
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ax), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+            }
+            __syncwarp();
+            if (p.dx) {  // this warp's 32 rows, four whole rows at a time
+                bf16* out = p.dx + static_cast<long long>(rg.first) * os + static_cast<long long>(h) * p.P + tile * kTile;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = quarter * 32 + k * 4 + (lane >> 3);
+                    uint4 v;
+                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(sx + tile_at<128>(r, lane & 7)) : "memory");
+                    if (r < valid) *reinterpret_cast<uint4*>(out + r * os + (lane & 7) * 8) = v;
+                }
+            }
+            mbar_arrive(emptied + 8 * (it & 1));
+            if (tile == p.tiles - 1) {
+                if (head >= 2 && !tc::wait_warp(sums_free + 8 * (head & 1), head / 2 - 1, p.flag)) break;
+                float* out = sums + (head & 1) * kSums;
+                out[kFin + row] = fin;
+                out[kDot + row] = dot;
+                mbar_arrive(sums_done + 8 * (head & 1));
+                fin = dot = 0.f;
+            }
+        }
+    } else if (threadIdx.x < kScorers + kWriters) {
+        // the rows' products of e with dout
+        float in = 0.f;
+        for (int it = 0; it < items; ++it) {
+            const int head = it / p.tiles, tile = it - head * p.tiles;
+            const float2 b = p.gb[(cells0 + h0 + head) * kChunk + row];
+            const uint32_t sy = stages + (it & 1) * 2 * Sh::kX + Sh::kX;
+            if (!tc::wait_warp(e_done, it, p.flag)) break;
+            tc::fence_after();
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                float e[8];
+                uint32_t y[4];
+                tc::tmem_ld8(e, tmem + kE + s * 8 + lanes);
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                             : "r"(sy + tile_at<128>(row, s)) : "memory");
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) in = fmaf(e[2 * k], lo_of(y[k]), fmaf(e[2 * k + 1], hi_of(y[k]), in));
+            }
+            tc::fence_before();
+            mbar_arrive(e_free);
+            mbar_arrive(emptied + 8 * (it & 1));
+            if (tile == p.tiles - 1) {
+                if (head >= 2 && !tc::wait_warp(sums_free + 8 * (head & 1), head / 2 - 1, p.flag)) break;
+                sums[(head & 1) * kSums + kIn + row] = in * ex2(b.x + b.y);
+                mbar_arrive(sums_done + 8 * (head & 1));
+                in = 0.f;
+            }
+        }
+    } else if (threadIdx.x < kScorers + kWriters + kConverters) {
+        // unit: rows 64 part .. of dS (even) or S_0 (odd) of a tile; this thread: row r, columns 16 c ..
+        const int i0 = threadIdx.x - kScorers - kWriters, r = i0 >> 2, c = i0 & 3, cw = i0 >> 5;
+        const int per_tile = 2 * (N / 64), total = items * per_tile;
+        auto source = [&](int u) {
+            const int it = u / per_tile, part = (u - it * per_tile) >> 1;
+            const long long cell = (cells0 + h0 + it / p.tiles) * p.tiles + it % p.tiles;
+            return reinterpret_cast<const float4*>(((u & 1) ? p.sf : p.df) + (cell * N + part * 64 + r) * kTile + c * 16);
+        };
+        float4 nx[4], ds[4];
+        auto read = [&](int u) {
+            if (u >= total) return;
+            const float4* s = source(u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) nx[k] = __ldg(s + k);
+        };
+        float through = 0.f;
+        read(0);
+        for (int u = 0; u < total; ++u) {
+            float4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = nx[k];
+            read(u + 1);
+            if (u & 1) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    through = fmaf(v[k].x, ds[k].x, fmaf(v[k].y, ds[k].y, fmaf(v[k].z, ds[k].z, fmaf(v[k].w, ds[k].w, through))));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) ds[k] = v[k];
+            }
+            if (u >= kUnits && !tc::wait_warp(unit_free + 8 * (u % kUnits), u / kUnits - 1, p.flag)) break;
+            const uint32_t to = units + (u % kUnits) * kUnit;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t t[3][4];
+                split3(v[2 * k].x, v[2 * k].y, t[0][0], t[1][0], t[2][0]);
+                split3(v[2 * k].z, v[2 * k].w, t[0][1], t[1][1], t[2][1]);
+                split3(v[2 * k + 1].x, v[2 * k + 1].y, t[0][2], t[1][2], t[2][2]);
+                split3(v[2 * k + 1].z, v[2 * k + 1].w, t[0][3], t[1][3], t[2][3]);
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + m * kPlane + tile_at<128>(r, 2 * c + k)), "r"(t[m][0]),
+                                 "r"(t[m][1]), "r"(t[m][2]), "r"(t[m][3])
+                                 : "memory");
+            }
+            tc::fence_smem();
+            mbar_arrive(unit_written + 8 * (u % kUnits));
+            const int head = u / (per_tile * p.tiles);
+            if (u == (head + 1) * per_tile * p.tiles - 1) {     // the head's last unit
+                if (head >= 2 && !tc::wait_warp(sums_free + 8 * (head & 1), head / 2 - 1, p.flag)) break;
+#pragma unroll
+                for (int d = 16; d; d >>= 1) through += __shfl_xor_sync(0xffffffffu, through, d);
+                if (lane == 0) sums[(head & 1) * kSums + kThrough + cw] = through;
+                __syncwarp();
+                mbar_arrive(sums_done + 8 * (head & 1));
+                through = 0.f;
+            }
+        }
+    } else if (threadIdx.x < kScorers + kWriters + kConverters + kLoaders) {
+        const int i0 = threadIdx.x - kScorers - kWriters - kConverters, t = i0 >> 3, c = i0 & 7;   // rows t + 8 j, columns 8 c ..
+        const uint32_t place = tile_at<128>(t, c);
+        auto rows = [&](uint32_t dst, const bf16* src, long long stride) {
+#pragma unroll 4
+            for (int j = 0; j < kChunk / 8; ++j) {
+                const bool on = t + 8 * j < valid;
+                cp16(dst + place + j * 1024, src + (on ? (t + 8 * j) * stride : 0) + c * 8, on);
+            }
+        };
+#pragma unroll
+        for (int b = 0; b < N / 64; ++b) {
+            rows(sb + b * kChunk * 128, p.Bm + rg.first * p.bs + group * N + b * 64, p.bs);
+            rows(sc + b * kChunk * 128, p.Cm + rg.first * p.cs + group * N + b * 64, p.cs);
+        }
+        cp_commit();
+        for (int it = 0; it <= items; ++it) {
+            if (it) {   // what was issued last is there
+                cp_wait<0>();
+                tc::fence_smem();
+                if (it == 1) mbar_arrive(keys);
+                mbar_arrive(loaded + 8 * ((it - 1) & 1));
+            }
+            if (it < items) {
+                if (it >= 2 && !tc::wait_warp(emptied + 8 * (it & 1), it / 2 - 1, p.flag)) break;
+                const int h = h0 + it / p.tiles, tile = it % p.tiles;
+                const uint32_t sx = stages + (it & 1) * 2 * Sh::kX;
+                rows(sx, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs);
+                rows(sx + Sh::kX, p.dout + rg.first * os + static_cast<long long>(h) * p.P + tile * kTile, os);
+            }
+            cp_commit();
+        }
+    } else if (warp == (kBlock >> 5) - 2) {
+        // a head's gates: lane l has tokens 4 l .. 4 l + 3
+        for (int i = 0; i < heads; ++i) {
+            const int h = h0 + i;
+            const float4 dt4 = *reinterpret_cast<const float4*>(p.gdt + (cells0 + h) * kChunk + lane * 4);
+            const float2 be = p.gb[(cells0 + h) * kChunk + kChunk - 1];
+            const float ah = p.decay ? 0.f : __ldg(p.A + h);
+            const float dt[4] = {dt4.x, dt4.y, dt4.z, dt4.w};
+            if (!tc::wait_warp(sums_done + 8 * (i & 1), i / 2, p.flag)) break;
+            const float* in = sums + (i & 1) * kSums;
+            float m[4], f[4], dir[4], dd = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = lane * 4 + k;
+                m[k] = f[k] = dir[k] = 0.f;
+                if (t >= valid) continue;
+                float z = 0.f;
+                for (int q = 0; q <= t / 32; ++q) z += in[kCol + q * 128 + t];
+                const float off = in[kRow + t] + in[kRow + 128 + t];
+                dir[k] = (off + in[kOwn + t]) + in[kFin + t];
+                m[k] = (z + in[kIn + t]) - dt[k] * off;
+                f[k] = dt[k] * in[kFin + t];
+                dd += in[kDot + t];
+            }
+            float thr = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) thr += in[kThrough + w];
+            thr *= ex2(be.x + be.y);
+            __syncwarp();
+            mbar_arrive(sums_free + 8 * (i & 1));
+            // m over the lanes behind this one, dt fin over the lanes before it
+            float after = __shfl_down_sync(0xffffffffu, m[0] + m[1] + m[2] + m[3], 1);
+            float before = __shfl_up_sync(0xffffffffu, f[0] + f[1] + f[2] + f[3], 1);
+            if (lane == 31) after = 0.f;
+            if (lane == 0) before = 0.f;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const float o = __shfl_down_sync(0xffffffffu, after, d), u = __shfl_up_sync(0xffffffffu, before, d);
+                if (lane + d < 32) after += o;
+                if (lane >= d) before += u;
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, d);
+            f[3] = before + f[0] + f[1] + f[2];   // now sums over the tokens before
+            f[2] = before + f[0] + f[1];
+            f[1] = before + f[0];
+            f[0] = before;
+            float da = 0.f, run = after;
+#pragma unroll
+            for (int k = 3; k >= 0; --k) {
+                const int t = lane * 4 + k;
+                run += m[k];
+                if (t >= valid) continue;
+                float dl = (run + f[k]) + thr;
+                const long long at = static_cast<long long>(rg.first + t) * p.H + h;
+                if (p.decay && __ldg(p.decay + at) == 0.f) dl = 0.f;  // nothing passes: the sums only cancel to rounding
+                if (p.dlog) p.dlog[at] = dl;
+                if (p.ddt) p.ddt[at] = p.decay ? dir[k] : fmaf(ah, dl, dir[k]);
+                da = fmaf(dt[k], dl, da);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) da += __shfl_xor_sync(0xffffffffu, da, d);
+            if (lane == 0) {
+                p.part[cells0 + h] = da;
+                p.part[static_cast<long long>(p.slots) * p.H + cells0 + h] = dd;
+            }
+        }
+    } else if (lane == 0) {
+        auto wait = [&](uint32_t b, int phase) { return mbar_wait(b, phase & 1, kWaitIters); };
+        bool ok = wait(keys, 0);
+        if (ok) {
+            tc::fence_after();
+            constexpr uint32_t id = tc::idesc(kChunk, false, false);
+#pragma unroll
+            for (int ks = 0; ks < N / 16; ++ks) {
+                const uint32_t o = (ks / 4) * kChunk * 128 + (ks % 4) * 32;
+                tc::mma(tmem + kG, tc::desc(sb + o, 16), tc::desc(sc + o, 16), id, ks);
+            }
+            tc::commit(g_done);
+        }
+        constexpr uint32_t id_w = tc::idesc(kChunk, false, false), id = tc::idesc(kTile, false, true);
+        int unit = 0;
+        for (int it = 0; it < items && ok; ++it) {
+            const int head = it / p.tiles, tile = it - head * p.tiles;
+            if (tile == 0) {
+                if (head && !(ok = wait(w_free, head - 1))) break;
+                for (int t = 0; t < p.tiles && ok; ++t) {
+                    if (!(ok = wait(loaded + 8 * ((it + t) & 1), (it + t) / 2))) break;
+                    tc::fence_after();
+                    const uint32_t sx = stages + ((it + t) & 1) * 2 * Sh::kX;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) tc::mma(tmem + kW, tc::desc(sx + ks * 32, 16), tc::desc(sx + Sh::kX + ks * 32, 16), id_w, t || ks);
+                }
+                if (!ok) break;
+                tc::commit(w_done);
+            }
+            if (it && !(ok = wait(cd_free, it - 1) && wait(e_free, it - 1))) break;
+            for (int part = 0; part < N / 64 && ok; ++part)
+                for (int which = 0; which < 2 && ok; ++which, ++unit) {
+                    if (!(ok = wait(unit_written + 8 * (unit % kUnits), unit / kUnits))) break;
+                    tc::fence_after();
+                    const uint32_t a = (which ? sc : sb) + part * kChunk * 128, b = units + (unit % kUnits) * kUnit;
+                    const uint32_t d = tmem + (which ? kE : kDd);
+#pragma unroll
+                    for (int m = 2; m >= 0; --m)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc::mma(d, tc::desc(a + ks * 32, 16), tc::desc(b + m * kPlane + ks * 2048, 16), id, part || m != 2 || ks);
+                    tc::commit(unit_free + 8 * (unit % kUnits));
+                }
+            if (!ok) break;
+            tc::commit(e_done);
+            if (tile == 0 && !(ok = wait(pt_written, head))) break;
+            tc::fence_after();
+            const uint32_t sy = stages + (it & 1) * 2 * Sh::kX + Sh::kX;
+#pragma unroll
+            for (int ks = 0; ks < kChunk / 16; ++ks) tc::mma_ta(tmem + kC, tmem + kPt + ks * 8, tc::desc(sy + ks * 2048, 16), id, ks);
+            tc::commit(cd_done);
+            if (tile == p.tiles - 1) tc::commit(pt_free);
+        }
+        if (!ok) atomicOr(p.flag, kFlagTimeout);
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) tc::tmem_free(tmem, 512);
+}
+
+template <int N>
+int run(const Params& p, int head_set, cudaStream_t s) {
+    const int err = cudaFuncSetAttribute(dx_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<N>::kSmem);
+    if (err) return err;
+    const dim3 grid(p.slots, p.G * ((p.per + head_set - 1) / head_set));
+    dx_tc_kernel<N><<<grid, kBlock, Shape<N>::kSmem, s>>>(p, head_set);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int launch_dx_tc(const Params& p, int head_set, cudaStream_t s) {
+    return p.N == 64 ? run<64>(p, head_set, s) : run<128>(p, head_set, s);
+}
+
+}  // namespace scan
+}  // namespace rsq

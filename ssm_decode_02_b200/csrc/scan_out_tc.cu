@@ -240,8 +240,12 @@ __global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant
             rows(sb + b * kChunk * 128, p.Bm + rg.first * p.bs + group * N + b * 64, p.bs, kChunk / 8, valid);
         }
         cp_commit();
-        // two stages are on their way while the one before them is waited for
+        // a stage is announced before the wait for room for the next but one: announcing it
+        // later would tie every tile to the writers of the tile two before it
         for (int it = 0; it <= items + 1; ++it) {
+            cp_wait<1>();
+            tc::fence_smem();
+            if (it) mbar_arrive(it == 1 ? keys : loaded + 8 * ((it - 2) % kStages));
             if (it < items) {
                 const int h = h0 + it / p.tiles, tile = it % p.tiles;
                 const uint32_t st = stages + (it % kStages) * Sh::kStage;
@@ -251,13 +255,6 @@ __global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant
                 rows(st + Sh::kX, p.sh + cell * N * kTile, kTile, N / 8, N);
             }
             cp_commit();
-            if (it == 1) continue;
-            if (it == 0)
-                cp_wait<1>();
-            else
-                cp_wait<2>();
-            tc::fence_smem();
-            mbar_arrive(it == 0 ? keys : loaded + 8 * ((it - 2) % kStages));
         }
         cp_wait<0>();
     } else if (lane == 0) {
