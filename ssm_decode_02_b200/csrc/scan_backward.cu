@@ -582,8 +582,12 @@ int backward_n(const Params& p, int head_set, cudaStream_t s) {
             err = cudaGetLastError();
         }
         if (!err && (p.dBm || p.dCm)) {
-            dk_kernel<N><<<dim3(p.slots, p.G * (N / DkShape<N>::kW), 2), kThreads, DkShape<N>::kSmem, s>>>(p);
-            err = cudaGetLastError();
+            if (dk_tc_ok(p)) {
+                err = launch_dk_tc(p, s);
+            } else {
+                dk_kernel<N><<<dim3(p.slots, p.G * (N / DkShape<N>::kW), 2), kThreads, DkShape<N>::kSmem, s>>>(p);
+                err = cudaGetLastError();
+            }
         }
         if (err) return err;
     }

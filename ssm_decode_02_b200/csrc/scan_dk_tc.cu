@@ -1,0 +1,328 @@
+// scan_dk_tc.cu -- dB and dC on the fifth-generation tensor cores (tcgen05): the form
+// of dk_kernel (scan_backward.cu) for dk of 64, 128 and 256 and dv of whole 64-column
+// tiles.
+//
+// A block takes one chunk, one group and 64 state rows, over all heads of the group:
+//     dC = sum_h 2^b (dout S_0^T) + M B,   dB = sum_h 2^(b_end-b) dt (x dS^T) + M^T C,
+//     M  = sum_h L . dt . (dout x^T)       (128 x 128 tokens, i >= j)
+// so that the products with the keys are two at the end, whatever the number of heads;
+// M is rounded to bf16 once, after the sum.  M lies in tensor memory, where the
+// scorers add to it; the other two sums lie in registers, a thread one row of 64.
+// Warps, which meet at mbarriers only:
+//   8 scorers, 4 + 4 summers, 4 converters (states to bf16), 2 loaders, 1 issuer.
+#include "tc.cuh"
+
+namespace rsq {
+namespace scan {
+namespace {
+
+constexpr int kScorers = 256, kSummers = 256, kConverters = 128, kLoaders = 64;
+constexpr int kBlock = kScorers + kSummers + kConverters + kLoaders + 32;
+constexpr int kUnits = 4;
+constexpr int kUnit = 64 * kTile * 2;
+constexpr int kX = kChunk * kTile * 2;
+constexpr int kW = 0, kM = 256, kT = 384;       // tensor memory: two of dout x^T, M, dout S^T and x dS^T
+constexpr int kSmem = 1024 + 4 * kX + kUnits * kUnit + 2 * kX + 2 * kX + 8 * 32 * (2 * 4 + 16) + 256;
+
+__global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant__ Params p) {
+    extern __shared__ uint8_t raw_smem[];
+    const Range rg = slot_range(p, blockIdx.x, kChunk);
+    if (!rg.valid) return;
+    const int parts = p.N / 64, group = blockIdx.y / parts, n0 = (blockIdx.y - group * parts) * 64;
+    const int h0 = group * p.per, heads = p.per, items = heads * p.tiles;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, valid = rg.valid;
+    const long long os = static_cast<long long>(p.H) * p.P, cells0 = static_cast<long long>(blockIdx.x) * p.H;
+
+    uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
+    const uint32_t stages = smem_u32(smem), units = stages + 4 * kX, sm = units + kUnits * kUnit, sk = sm + 2 * kX;  // sk: B, C
+    float* facs = reinterpret_cast<float*>(smem + 8 * kX + kUnits * kUnit);   // [8 warps][2][32]
+    float4* pairs = reinterpret_cast<float4*>(facs + 8 * 64);                  // [8 warps][32]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pairs + 8 * 32);
+    uint32_t bar = smem_u32(tmem_slot + 2);
+    auto next_bar = [&](int n) {
+        const uint32_t b = bar;
+        bar += 8 * n;
+        return b;
+    };
+    const uint32_t keys = next_bar(1), loaded = next_bar(2), emptied = next_bar(2), unit_written = next_bar(kUnits),
+                   unit_free = next_bar(kUnits), w_done = next_bar(2), w_free = next_bar(2), t_done = next_bar(1), t_free = next_bar(1),
+                   m_written = next_bar(1), f_done = next_bar(1);
+    if (warp == 0) tc::tmem_alloc(smem_u32(tmem_slot), 512);
+    if (threadIdx.x == 0) {
+        mbar_init(keys, kLoaders);
+        mbar_init(t_done, 1);
+        mbar_init(t_free, kSummers);
+        mbar_init(m_written, kScorers);
+        mbar_init(f_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(loaded + 8 * i, kLoaders);
+            mbar_init(emptied + 8 * i, 1);
+            mbar_init(w_done + 8 * i, 1);
+            mbar_init(w_free + 8 * i, kScorers);
+        }
+        for (int i = 0; i < kUnits; ++i) {
+            mbar_init(unit_written + 8 * i, kConverters);
+            mbar_init(unit_free + 8 * i, 1);
+        }
+        fence_mbar_init();
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *tmem_slot, lanes = (static_cast<uint32_t>(warp) & 3) << 21;
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+
+    if (threadIdx.x < kScorers) {
+        const int half = warp >> 2;                             // columns 64 half ..
+        float* fac = facs + warp * 64;
+        float4* pair = pairs + warp * 32;
+        const bool any = half * 2 <= quarter;
+        float2 nc[2] = {}, nr = make_float2(0.f, 0.f);
+        float nd[2] = {};
+        auto read = [&](int i) {
+            if (i >= heads || !any) return;
+            const long long at = (cells0 + h0 + i) * kChunk;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                nc[k] = p.gb[at + half * 64 + k * 32 + lane];
+                nd[k] = p.gdt[at + half * 64 + k * 32 + lane];
+            }
+            nr = p.gb[at + row];
+        };
+        read(0);
+        bool ok = true;
+        for (int i = 0; i < heads; ++i) {
+            const float2 bc[2] = {nc[0], nc[1]}, br = nr;
+            const float dt[2] = {nd[0], nd[1]};
+            read(i + 1);
+            if (!(ok = tc::wait_warp(w_done + 8 * (i & 1), i / 2, p.flag))) break;
+            tc::fence_after();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int cols = half * 2 + k;
+                if (cols > quarter) continue;                   // behind every row
+                const bool diagonal = cols == quarter;
+                const int meet = diagonal ? 0 : 31;
+                const float2 bm = make_float2(__shfl_sync(0xffffffffu, bc[k].x, meet), __shfl_sync(0xffffffffu, bc[k].y, meet));
+                const float last = __shfl_sync(0xffffffffu, bc[k].x, 31);
+                const float r = ex2_diff(br, bm);
+                const bool direct = diagonal && !(bm.x - last < 60.f);
+                __syncwarp();
+                fac[k * 32 + lane] = dt[k] * ex2_diff(bm, bc[k]);
+                if (direct) pair[lane] = make_float4(bc[k].x, bc[k].y, dt[k], 0.f);
+                __syncwarp();
+                const uint32_t src = tmem + kW + (i & 1) * 128 + cols * 32 + lanes, dst = tmem + kM + cols * 32 + lanes;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    float w[8], m[8];
+                    tc::tmem_ld8(w, src + s * 8);
+                    if (i) tc::tmem_ld8(m, dst + s * 8);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int c = s * 8 + q;
+                        float f;
+                        if (!direct) {
+                            f = r * fac[k * 32 + c];
+                        } else {
+                            const float4 e = pair[c];
+                            f = ex2_diff(br, c <= lane ? make_float2(e.x, e.y) : br) * e.z;
+                        }
+                        if (diagonal && c > lane) f = 0.f, w[q] = 0.f;
+                        m[q] = i ? fmaf(w[q], f, m[q]) : w[q] * f;
+                    }
+                    uint32_t o[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(m[q]);
+                    tc::tmem_st8(dst + s * 8, o);
+                }
+            }
+            tc::tmem_st_wait();
+            tc::fence_before();
+            mbar_arrive(w_free + 8 * (i & 1));
+        }
+        // M as bf16 rows: the left operand, and transposed
+        if (ok) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int cols = half * 2 + s / 4;
+                float m[8];
+                if (cols <= quarter) {
+                    tc::tmem_ld8(m, tmem + kM + half * 64 + s * 8 + lanes);
+                    tc::tmem_ld_wait();
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) m[q] = 0.f;
+                }
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sm + half * kX + tile_at<128>(row, s)), "r"(pack(m[0], m[1])),
+                             "r"(pack(m[2], m[3])), "r"(pack(m[4], m[5])), "r"(pack(m[6], m[7]))
+                             : "memory");
+            }
+            tc::fence_smem();
+            mbar_arrive(m_written);
+        }
+    } else if (threadIdx.x < kScorers + kSummers) {
+        const int key = (warp - kScorers / 32) >> 2;            // 0: dC, 1: dB
+        bf16* out = key ? p.dBm : p.dCm;
+        float tot[64];
+#pragma unroll
+        for (int k = 0; k < 64; ++k) tot[k] = 0.f;
+        float2 nb = make_float2(0.f, 0.f), ne = nb;
+        float nd = 0.f;
+        auto read = [&](int i) {
+            if (i >= heads) return;
+            const long long at = (cells0 + h0 + i) * kChunk;
+            nb = p.gb[at + row];
+            if (key) {
+                ne = p.gb[at + kChunk - 1];
+                nd = p.gdt[at + row];
+            }
+        };
+        read(0);
+        bool ok = true;
+        for (int i = 0; i <= heads && ok; ++i) {
+            const float w = i == heads ? 1.f : (key ? ex2_diff(ne, nb) * nd : ex2(nb.x + nb.y));
+            read(i + 1);
+            // after the heads' products the one with M
+            if (!(ok = tc::wait_warp(i < heads ? t_done : f_done, i < heads ? i : 0, p.flag))) break;
+            tc::fence_after();
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                float t[8];
+                tc::tmem_ld8(t, tmem + kT + key * 64 + s * 8 + lanes);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) tot[s * 8 + k] = fmaf(w, t[k], tot[s * 8 + k]);
+            }
+            tc::fence_before();
+            if (i < heads) mbar_arrive(t_free);
+        }
+        if (ok && out && row < valid) {
+            out += (static_cast<long long>(rg.first + row) * p.G + group) * p.N + n0;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                *reinterpret_cast<uint4*>(out + s * 8) = make_uint4(pack(tot[s * 8], tot[s * 8 + 1]), pack(tot[s * 8 + 2], tot[s * 8 + 3]),
+                                                                    pack(tot[s * 8 + 4], tot[s * 8 + 5]), pack(tot[s * 8 + 6], tot[s * 8 + 7]));
+        }
+    } else if (threadIdx.x < kScorers + kSummers + kConverters) {
+        // unit: the block's 64 rows of S_0 (even) or dS (odd) of a tile; rows r + 16 k, columns 8 c ..
+        const int i0 = threadIdx.x - kScorers - kSummers, r = i0 >> 3, c = i0 & 7;
+        float4 nx[8];
+        auto read = [&](int u) {
+            if (u >= 2 * items) return;
+            const int it = u >> 1;
+            const long long cell = (cells0 + h0 + it / p.tiles) * p.tiles + it % p.tiles;
+            const float4* s = reinterpret_cast<const float4*>(((u & 1) ? p.df : p.sf) + (cell * p.N + n0 + r) * kTile + c * 8);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                nx[2 * k] = __ldg(s + k * 16 * kTile / 4);
+                nx[2 * k + 1] = __ldg(s + k * 16 * kTile / 4 + 1);
+            }
+        };
+        read(0);
+        for (int u = 0; u < 2 * items; ++u) {
+            uint32_t o[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                o[k][0] = pack(nx[2 * k].x, nx[2 * k].y);
+                o[k][1] = pack(nx[2 * k].z, nx[2 * k].w);
+                o[k][2] = pack(nx[2 * k + 1].x, nx[2 * k + 1].y);
+                o[k][3] = pack(nx[2 * k + 1].z, nx[2 * k + 1].w);
+            }
+            read(u + 1);
+            if (u >= kUnits && !tc::wait_warp(unit_free + 8 * (u % kUnits), u / kUnits - 1, p.flag)) break;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(units + (u % kUnits) * kUnit + tile_at<128>(r + 16 * k, c)),
+                             "r"(o[k][0]), "r"(o[k][1]), "r"(o[k][2]), "r"(o[k][3])
+                             : "memory");
+            tc::fence_smem();
+            mbar_arrive(unit_written + 8 * (u % kUnits));
+        }
+    } else if (threadIdx.x < kScorers + kSummers + kConverters + kLoaders) {
+        const int i0 = threadIdx.x - kScorers - kSummers - kConverters, t = i0 >> 3, c = i0 & 7;   // rows t + 8 j, columns 8 c ..
+        const uint32_t place = tile_at<128>(t, c);
+        auto rows = [&](uint32_t dst, const bf16* src, long long stride) {
+#pragma unroll 4
+            for (int j = 0; j < kChunk / 8; ++j) {
+                const bool on = t + 8 * j < valid;
+                cp16(dst + place + j * 1024, src + (on ? (t + 8 * j) * stride : 0) + c * 8, on);
+            }
+        };
+        rows(sk, p.Bm + rg.first * p.bs + group * p.N + n0, p.bs);
+        rows(sk + kX, p.Cm + rg.first * p.cs + group * p.N + n0, p.cs);
+        cp_commit();
+        for (int it = 0; it <= items; ++it) {
+            if (it) {   // what was issued last is there
+                cp_wait<0>();
+                tc::fence_smem();
+                if (it == 1) mbar_arrive(keys);
+                mbar_arrive(loaded + 8 * ((it - 1) & 1));
+            }
+            if (it < items) {
+                if (it >= 2 && !tc::wait_warp(emptied + 8 * (it & 1), it / 2 - 1, p.flag)) break;
+                const int h = h0 + it / p.tiles, tile = it % p.tiles;
+                const uint32_t sx = stages + (it & 1) * 2 * kX;
+                rows(sx, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs);
+                rows(sx + kX, p.dout + rg.first * os + static_cast<long long>(h) * p.P + tile * kTile, os);
+            }
+            cp_commit();
+        }
+    } else if (lane == 0) {
+        auto wait = [&](uint32_t b, int phase) { return mbar_wait(b, phase & 1, kWaitIters); };
+        bool ok = true;
+        constexpr uint32_t id_w = tc::idesc(kChunk, false, false), id_t = tc::idesc(64, false, false);
+        for (int it = 0; it < items && ok; ++it) {
+            const int head = it / p.tiles, tile = it - head * p.tiles;
+            if (!(ok = wait(loaded + 8 * (it & 1), it / 2))) break;
+            if (tile == 0 && head >= 2 && !(ok = wait(w_free + 8 * (head & 1), head / 2 - 1))) break;
+            tc::fence_after();
+            const uint32_t sx = stages + (it & 1) * 2 * kX, sy = sx + kX, w = tmem + kW + (head & 1) * 128;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) tc::mma(w, tc::desc(sy + ks * 32, 16), tc::desc(sx + ks * 32, 16), id_w, tile || ks);
+            if (tile == p.tiles - 1) tc::commit(w_done + 8 * (head & 1));
+            if (tile == 0 && head && !(ok = wait(t_free, head - 1))) break;
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                const int u = 2 * it + which;
+                if (!(ok = wait(unit_written + 8 * (u % kUnits), u / kUnits))) break;
+                tc::fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    tc::mma(tmem + kT + which * 64, tc::desc((which ? sx : sy) + ks * 32, 16),
+                            tc::desc(units + (u % kUnits) * kUnit + ks * 32, 16), id_t, tile || ks);
+                tc::commit(unit_free + 8 * (u % kUnits));
+            }
+            if (!ok) break;
+            tc::commit(emptied + 8 * (it & 1));
+            if (tile == p.tiles - 1) tc::commit(t_done);
+        }
+        if (ok && (ok = wait(keys, 0) && wait(m_written, 0) && wait(t_free, heads - 1))) {
+            tc::fence_after();
+            constexpr uint32_t id_c = tc::idesc(64, false, true), id_b = tc::idesc(64, true, true);
+#pragma unroll
+            for (int ks = 0; ks < kChunk / 16; ++ks)
+                tc::mma(tmem + kT, tc::desc(sm + (ks / 4) * kX + (ks % 4) * 32, 16), tc::desc(sk + ks * 2048, 16), id_c, ks);
+#pragma unroll
+            for (int ks = 0; ks < kChunk / 16; ++ks)
+                tc::mma(tmem + kT + 64, tc::desc(sm + ks * 2048, kX), tc::desc(sk + kX + ks * 2048, 16), id_b, ks);
+            tc::commit(f_done);
+        }
+        if (!ok) atomicOr(p.flag, kFlagTimeout);
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) tc::tmem_free(tmem, 512);
+}
+
+}  // namespace
+
+int launch_dk_tc(const Params& p, cudaStream_t s) {
+    const int err = cudaFuncSetAttribute(dk_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (err) return err;
+    dk_tc_kernel<<<dim3(p.slots, p.G * (p.N / 64)), kBlock, kSmem, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace scan
+}  // namespace rsq
