@@ -16,13 +16,15 @@ namespace rsq {
 namespace scan {
 namespace {
 
-constexpr int kScorers = 256, kSummers = 256, kConverters = 128, kLoaders = 64;
+constexpr int kScorers = 256, kSummers = 256, kConverters = 128, kLoaders = 96;
 constexpr int kBlock = kScorers + kSummers + kConverters + kLoaders + 32;
-constexpr int kUnits = 4;
-constexpr int kUnit = 64 * kTile * 2;
+constexpr int kStages = 3;                      // of x and dout, a loader warp each
+constexpr int kUnits = 4, kRaws = 4;            // rings of 64 state rows in bf16, and in binary32 on their way
+constexpr int kUnit = 64 * kTile * 2, kRaw = 64 * kTile * 4;
 constexpr int kX = kChunk * kTile * 2;
 constexpr int kW = 0, kM = 256, kT = 384;       // tensor memory: two of dout x^T, M, dout S^T and x dS^T
-constexpr int kSmem = 1024 + 4 * kX + kUnits * kUnit + 2 * kX + 2 * kX + 8 * 32 * (2 * 4 + 16) + 256;
+// M and the keys come where the stages were
+constexpr int kSmem = 1024 + kStages * 2 * kX + kUnits * kUnit + kRaws * kRaw + 8 * 32 * (2 * 4 + 16) + 384;
 
 __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant__ Params p) {
     extern __shared__ uint8_t raw_smem[];
@@ -34,8 +36,9 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
     const long long os = static_cast<long long>(p.H) * p.P, cells0 = static_cast<long long>(blockIdx.x) * p.H;
 
     uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
-    const uint32_t stages = smem_u32(smem), units = stages + 4 * kX, sm = units + kUnits * kUnit, sk = sm + 2 * kX;  // sk: B, C
-    float* facs = reinterpret_cast<float*>(smem + 8 * kX + kUnits * kUnit);   // [8 warps][2][32]
+    const uint32_t stages = smem_u32(smem), units = stages + kStages * 2 * kX, raws = units + kUnits * kUnit;
+    const uint32_t sm = stages, sk = sm + 2 * kX;  // after the last head: M; B, C
+    float* facs = reinterpret_cast<float*>(smem + kStages * 2 * kX + kUnits * kUnit + kRaws * kRaw);   // [8 warps][2][32]
     float4* pairs = reinterpret_cast<float4*>(facs + 8 * 64);                  // [8 warps][32]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pairs + 8 * 32);
     uint32_t bar = smem_u32(tmem_slot + 2);
@@ -44,19 +47,26 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
         bar += 8 * n;
         return b;
     };
-    const uint32_t keys = next_bar(1), loaded = next_bar(2), emptied = next_bar(2), unit_written = next_bar(kUnits),
+    const uint32_t keys = next_bar(1), loaded = next_bar(kStages), emptied = next_bar(kStages), unit_written = next_bar(kUnits),
                    unit_free = next_bar(kUnits), w_done = next_bar(2), w_free = next_bar(2), t_done = next_bar(1), t_free = next_bar(1),
-                   m_written = next_bar(1), f_done = next_bar(1);
+                   m_written = next_bar(1), f_done = next_bar(1), heads_done = next_bar(1), raw_done = next_bar(kRaws), raw_free = next_bar(kRaws);
     if (warp == 0) tc::tmem_alloc(smem_u32(tmem_slot), 512);
     if (threadIdx.x == 0) {
-        mbar_init(keys, kLoaders);
+        mbar_init(keys, 64);
         mbar_init(t_done, 1);
         mbar_init(t_free, kSummers);
         mbar_init(m_written, kScorers);
         mbar_init(f_done, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(loaded + 8 * i, kLoaders);
+        mbar_init(heads_done, 1);
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(loaded + 8 * i, 32);
             mbar_init(emptied + 8 * i, 1);
+        }
+        for (int i = 0; i < kRaws; ++i) {
+            mbar_init(raw_done + 8 * i, 1);
+            mbar_init(raw_free + 8 * i, kConverters);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(w_done + 8 * i, 1);
             mbar_init(w_free + 8 * i, kScorers);
         }
@@ -113,36 +123,49 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
                 __syncwarp();
                 const uint32_t src = tmem + kW + (i & 1) * 128 + cols * 32 + lanes, dst = tmem + kM + cols * 32 + lanes;
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    float w[8], m[8];
-                    tc::tmem_ld8(w, src + s * 8);
-                    if (i) tc::tmem_ld8(m, dst + s * 8);
+                for (int s = 0; s < 2; ++s) {
+                    float w[16], m[16];
+                    tc::tmem_ld16(w, src + s * 16);
+                    if (i)
+                        tc::tmem_ld16(m, dst + s * 16);
+                    else
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) m[q] = 0.f;
                     tc::tmem_ld_wait();
+                    if (direct) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int c = s * 8 + q;
-                        float f;
-                        if (!direct) {
-                            f = r * fac[k * 32 + c];
-                        } else {
+                        for (int q = 0; q < 16; ++q) {
+                            const int c = s * 16 + q;
                             const float4 e = pair[c];
-                            f = ex2_diff(br, c <= lane ? make_float2(e.x, e.y) : br) * e.z;
+                            const float f = c <= lane ? ex2_diff(br, make_float2(e.x, e.y)) * e.z : 0.f;
+                            m[q] = fmaf(c <= lane ? w[q] : 0.f, f, m[q]);
                         }
-                        if (diagonal && c > lane) f = 0.f, w[q] = 0.f;
-                        m[q] = i ? fmaf(w[q], f, m[q]) : w[q] * f;
-                    }
-                    uint32_t o[8];
+                    } else {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) o[q] = __float_as_uint(m[q]);
-                    tc::tmem_st8(dst + s * 8, o);
+                        for (int q = 0; q < 4; ++q) {
+                            const float4 f = reinterpret_cast<const float4*>(fac + k * 32)[s * 4 + q];
+                            w[4 * q] *= r * f.x;
+                            w[4 * q + 1] *= r * f.y;
+                            w[4 * q + 2] *= r * f.z;
+                            w[4 * q + 3] *= r * f.w;
+                        }
+                        if (diagonal) {
+#pragma unroll
+                            for (int q = 0; q < 16; ++q) w[q] = s * 16 + q <= lane ? w[q] : 0.f;
+                        }
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) m[q] += w[q];
+                    }
+                    tc::tmem_st16(dst + s * 16, reinterpret_cast<const uint32_t(&)[16]>(m));
                 }
             }
             tc::tmem_st_wait();
             tc::fence_before();
             mbar_arrive(w_free + 8 * (i & 1));
         }
-        // M as bf16 rows: the left operand, and transposed
-        if (ok) {
+        // M as bf16 rows where the stages were, once every product is done with them: the
+        // left operand, and transposed
+        if (ok && (ok = tc::wait_warp(heads_done, 0, p.flag))) {
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
                 const int cols = half * 2 + s / 4;
@@ -205,68 +228,76 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
                                                                     pack(tot[s * 8 + 4], tot[s * 8 + 5]), pack(tot[s * 8 + 6], tot[s * 8 + 7]));
         }
     } else if (threadIdx.x < kScorers + kSummers + kConverters) {
-        // unit: the block's 64 rows of S_0 (even) or dS (odd) of a tile; rows r + 16 k, columns 8 c ..
-        const int i0 = threadIdx.x - kScorers - kSummers, r = i0 >> 3, c = i0 & 7;
-        float4 nx[8];
-        auto read = [&](int u) {
-            if (u >= 2 * items) return;
+        // unit: the block's 64 rows of S_0 (even) or dS (odd) of a tile, 16 KB in a row in
+        // memory, copied whole; this thread: rows r + 8 k, columns 4 c ..
+        const int i0 = threadIdx.x - kScorers - kSummers, r = i0 >> 4, c = i0 & 15, total = 2 * items;
+        auto fetch = [&](int u) {
             const int it = u >> 1;
             const long long cell = (cells0 + h0 + it / p.tiles) * p.tiles + it % p.tiles;
-            const float4* s = reinterpret_cast<const float4*>(((u & 1) ? p.df : p.sf) + (cell * p.N + n0 + r) * kTile + c * 8);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                nx[2 * k] = __ldg(s + k * 16 * kTile / 4);
-                nx[2 * k + 1] = __ldg(s + k * 16 * kTile / 4 + 1);
-            }
+            const uint32_t b = raw_done + 8 * (u % kRaws);
+            mbar_arrive_expect_tx(b, kRaw);
+            bulk_g2s(raws + (u % kRaws) * kRaw, ((u & 1) ? p.df : p.sf) + (cell * p.N + n0) * kTile, kRaw, b);
         };
-        read(0);
-        for (int u = 0; u < 2 * items; ++u) {
-            uint32_t o[4][4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                o[k][0] = pack(nx[2 * k].x, nx[2 * k].y);
-                o[k][1] = pack(nx[2 * k].z, nx[2 * k].w);
-                o[k][2] = pack(nx[2 * k + 1].x, nx[2 * k + 1].y);
-                o[k][3] = pack(nx[2 * k + 1].z, nx[2 * k + 1].w);
-            }
-            read(u + 1);
+        if (i0 == 0)
+            for (int u = 0; u < min(kRaws, total); ++u) fetch(u);
+        int u = 0;
+        for (; u < total; ++u) {
+            if (!tc::wait_warp(raw_done + 8 * (u % kRaws), u / kRaws, p.flag)) break;
             if (u >= kUnits && !tc::wait_warp(unit_free + 8 * (u % kUnits), u / kUnits - 1, p.flag)) break;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(units + (u % kUnits) * kUnit + tile_at<128>(r + 16 * k, c)),
-                             "r"(o[k][0]), "r"(o[k][1]), "r"(o[k][2]), "r"(o[k][3])
+            for (int k = 0; k < 8; ++k) {
+                float4 v;
+                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                             : "r"(raws + (u % kRaws) * kRaw + (r + 8 * k) * kTile * 4 + c * 16) : "memory");
+                asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(units + (u % kUnits) * kUnit + tile_at<128>(r + 8 * k, c >> 1) + 8 * (c & 1)),
+                             "r"(pack(v.x, v.y)), "r"(pack(v.z, v.w))
                              : "memory");
+            }
+            mbar_arrive(raw_free + 8 * (u % kRaws));
             tc::fence_smem();
             mbar_arrive(unit_written + 8 * (u % kUnits));
+            if (i0 == 0 && u + kRaws < total) {
+                if (mbar_wait(raw_free + 8 * (u % kRaws), (u / kRaws) & 1, kWaitIters))
+                    fetch(u + kRaws);
+                else
+                    atomicOr(p.flag, kFlagTimeout);
+            }
+            __syncwarp();
         }
+        // left early: no copy may still be on its way when the block ends
+        if (i0 == 0)
+            for (int v = u; v < min(u + kRaws, total); ++v) mbar_wait(raw_done + 8 * (v % kRaws), (v / kRaws) & 1, kDrainIters);
     } else if (threadIdx.x < kScorers + kSummers + kConverters + kLoaders) {
-        const int i0 = threadIdx.x - kScorers - kSummers - kConverters, t = i0 >> 3, c = i0 & 7;   // rows t + 8 j, columns 8 c ..
-        const uint32_t place = tile_at<128>(t, c);
+        // a warp for each stage: rows t + 4 j, columns 8 c ..
+        const int mine = warp - (kScorers + kSummers + kConverters) / 32, t = lane >> 3, c = lane & 7;
         auto rows = [&](uint32_t dst, const bf16* src, long long stride) {
-#pragma unroll 4
-            for (int j = 0; j < kChunk / 8; ++j) {
-                const bool on = t + 8 * j < valid;
-                cp16(dst + place + j * 1024, src + (on ? (t + 8 * j) * stride : 0) + c * 8, on);
+#pragma unroll 8
+            for (int j = 0; j < kChunk / 4; ++j) {
+                const bool on = t + 4 * j < valid;
+                cp16(dst + tile_at<128>(t + 4 * (j & 1), c) + (j >> 1) * 1024, src + (on ? (t + 4 * j) * stride : 0) + c * 8, on);
             }
         };
-        rows(sk, p.Bm + rg.first * p.bs + group * p.N + n0, p.bs);
-        rows(sk + kX, p.Cm + rg.first * p.cs + group * p.N + n0, p.cs);
-        cp_commit();
-        for (int it = 0; it <= items; ++it) {
-            if (it) {   // what was issued last is there
-                cp_wait<0>();
-                tc::fence_smem();
-                if (it == 1) mbar_arrive(keys);
-                mbar_arrive(loaded + 8 * ((it - 1) & 1));
-            }
-            if (it < items) {
-                if (it >= 2 && !tc::wait_warp(emptied + 8 * (it & 1), it / 2 - 1, p.flag)) break;
-                const int h = h0 + it / p.tiles, tile = it % p.tiles;
-                const uint32_t sx = stages + (it & 1) * 2 * kX;
-                rows(sx, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs);
-                rows(sx + kX, p.dout + rg.first * os + static_cast<long long>(h) * p.P + tile * kTile, os);
-            }
+        bool ok = true;
+        for (int it = mine; it < items; it += kStages) {
+            if (it >= kStages && !(ok = tc::wait_warp(emptied + 8 * mine, it / kStages - 1, p.flag))) break;
+            const int h = h0 + it / p.tiles, tile = it % p.tiles;
+            const uint32_t sx = stages + mine * 2 * kX;
+            rows(sx, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs);
+            rows(sx + kX, p.dout + rg.first * os + static_cast<long long>(h) * p.P + tile * kTile, os);
             cp_commit();
+            cp_wait<0>();
+            tc::fence_smem();
+            mbar_arrive(loaded + 8 * mine);
+        }
+        if (mine < 2 && ok && tc::wait_warp(heads_done, 0, p.flag)) {
+            if (mine == 0)
+                rows(sk, p.Bm + rg.first * p.bs + group * p.N + n0, p.bs);
+            else
+                rows(sk + kX, p.Cm + rg.first * p.cs + group * p.N + n0, p.cs);
+            cp_commit();
+            cp_wait<0>();
+            tc::fence_smem();
+            mbar_arrive(keys);
         }
     } else if (lane == 0) {
         auto wait = [&](uint32_t b, int phase) { return mbar_wait(b, phase & 1, kWaitIters); };
@@ -274,10 +305,10 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
         constexpr uint32_t id_w = tc::idesc(kChunk, false, false), id_t = tc::idesc(64, false, false);
         for (int it = 0; it < items && ok; ++it) {
             const int head = it / p.tiles, tile = it - head * p.tiles;
-            if (!(ok = wait(loaded + 8 * (it & 1), it / 2))) break;
+            if (!(ok = wait(loaded + 8 * (it % kStages), it / kStages))) break;
             if (tile == 0 && head >= 2 && !(ok = wait(w_free + 8 * (head & 1), head / 2 - 1))) break;
             tc::fence_after();
-            const uint32_t sx = stages + (it & 1) * 2 * kX, sy = sx + kX, w = tmem + kW + (head & 1) * 128;
+            const uint32_t sx = stages + (it % kStages) * 2 * kX, sy = sx + kX, w = tmem + kW + (head & 1) * 128;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) tc::mma(w, tc::desc(sy + ks * 32, 16), tc::desc(sx + ks * 32, 16), id_w, tile || ks);
             if (tile == p.tiles - 1) tc::commit(w_done + 8 * (head & 1));
@@ -294,9 +325,10 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
                 tc::commit(unit_free + 8 * (u % kUnits));
             }
             if (!ok) break;
-            tc::commit(emptied + 8 * (it & 1));
+            tc::commit(emptied + 8 * (it % kStages));
             if (tile == p.tiles - 1) tc::commit(t_done);
         }
+        if (ok) tc::commit(heads_done);
         if (ok && (ok = wait(keys, 0) && wait(m_written, 0) && wait(t_free, heads - 1))) {
             tc::fence_after();
             constexpr uint32_t id_c = tc::idesc(64, false, true), id_b = tc::idesc(64, true, true);

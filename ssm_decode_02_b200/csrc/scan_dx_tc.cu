@@ -25,7 +25,8 @@ namespace {
 
 constexpr int kScorers = 256, kWriters = 256, kConverters = 256, kLoaders = 64;
 constexpr int kBlock = kScorers + kWriters + kConverters + kLoaders + 64;
-constexpr int kUnits = 3;                       // ring of 64 state rows in three terms
+constexpr int kUnits = 2;                       // ring of 64 state rows in three terms
+constexpr int kRaw = 64 * kTile * 4;            // the same rows in binary32, two on their way
 constexpr int kPlane = 64 * kTile * 2, kUnit = 3 * kPlane;
 constexpr int kG = 0, kW = 128, kC = 256, kDd = 320, kE = 384, kPt = 448;
 // sums of one head (floats)
@@ -35,7 +36,7 @@ template <int N>
 struct Shape {
     static constexpr int kKeys = kChunk * N * 2;
     static constexpr int kX = kChunk * kTile * 2;
-    static constexpr int kSmem = 1024 + 2 * kKeys + 4 * kX + kUnits * kUnit + 8 * 32 * (2 * 4 + 8) + 2 * kSums * 4 + 256;
+    static constexpr int kSmem = 1024 + 2 * kKeys + 4 * kX + kUnits * kUnit + 2 * kRaw + 8 * 32 * (2 * 4 + 8) + 2 * kSums * 4 + 256;
 };
 
 // v[k] of the 32 lanes added up; lane l gets the sum of v[l].
@@ -74,8 +75,8 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
     const long long os = static_cast<long long>(p.H) * p.P;
 
     uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
-    const uint32_t sb = smem_u32(smem), sc = sb + Sh::kKeys, stages = sc + Sh::kKeys, units = stages + 4 * Sh::kX;
-    float* facs = reinterpret_cast<float*>(smem + 2 * Sh::kKeys + 4 * Sh::kX + kUnits * kUnit);   // [8 warps][2][32]
+    const uint32_t sb = smem_u32(smem), sc = sb + Sh::kKeys, stages = sc + Sh::kKeys, units = stages + 4 * Sh::kX, raws = units + kUnits * kUnit;
+    float* facs = reinterpret_cast<float*>(smem + 2 * Sh::kKeys + 4 * Sh::kX + kUnits * kUnit + 2 * kRaw);   // [8 warps][2][32]
     float2* pairs = reinterpret_cast<float2*>(facs + 8 * 64);                                      // [8 warps][32]
     float* sums = reinterpret_cast<float*>(pairs + 8 * 32);                                        // [2][kSums]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums + 2 * kSums);
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
     const uint32_t keys = next_bar(1), g_done = next_bar(1), loaded = next_bar(2), emptied = next_bar(2), unit_written = next_bar(kUnits),
                    unit_free = next_bar(kUnits), w_done = next_bar(1), w_free = next_bar(1), pt_written = next_bar(1),
                    pt_free = next_bar(1), cd_done = next_bar(1), cd_free = next_bar(1), e_done = next_bar(1), e_free = next_bar(1),
-                   sums_done = next_bar(2), sums_free = next_bar(2);
+                   sums_done = next_bar(2), sums_free = next_bar(2), raw_done = next_bar(2), raw_free = next_bar(2);
     if (warp == 0) tc::tmem_alloc(smem_u32(tmem_slot), 512);
     if (threadIdx.x == 0) {
         mbar_init(keys, kLoaders);
@@ -100,7 +101,9 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
             mbar_init(unit_free + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(loaded + 8 * i, kLoaders);
+            mbar_init(loaded + 8 * i, 32);
+            mbar_init(raw_done + 8 * i, 1);
+            mbar_init(raw_free + 8 * i, kConverters);
             mbar_init(emptied + 8 * i, kWriters);
             mbar_init(sums_done + 8 * i, kScorers + kWriters + kConverters);
             mbar_init(sums_free + 8 * i, 32);
@@ -309,28 +312,29 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
             }
         }
     } else if (threadIdx.x < kScorers + kWriters + kConverters) {
-        // unit: rows 64 part .. of dS (even) or S_0 (odd) of a tile; this thread: row r, columns 16 c ..
-        const int i0 = threadIdx.x - kScorers - kWriters, r = i0 >> 2, c = i0 & 3, cw = i0 >> 5;
+        // unit: rows 64 part .. of dS (even) or S_0 (odd) of a tile, 16 KB in a row in memory,
+        // copied whole; this thread: rows r + 16 k, columns 4 c ..
+        const int i0 = threadIdx.x - kScorers - kWriters, r = i0 >> 4, c = i0 & 15, cw = i0 >> 5;
         const int per_tile = 2 * (N / 64), total = items * per_tile;
-        auto source = [&](int u) {
+        auto fetch = [&](int u) {
             const int it = u / per_tile, part = (u - it * per_tile) >> 1;
             const long long cell = (cells0 + h0 + it / p.tiles) * p.tiles + it % p.tiles;
-            return reinterpret_cast<const float4*>(((u & 1) ? p.sf : p.df) + (cell * N + part * 64 + r) * kTile + c * 16);
+            mbar_arrive_expect_tx(raw_done + 8 * (u & 1), kRaw);
+            bulk_g2s(raws + (u & 1) * kRaw, ((u & 1) ? p.sf : p.df) + (cell * N + part * 64) * kTile, kRaw, raw_done + 8 * (u & 1));
         };
-        float4 nx[4], ds[4];
-        auto read = [&](int u) {
-            if (u >= total) return;
-            const float4* s = source(u);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) nx[k] = __ldg(s + k);
-        };
+        if (i0 == 0)
+            for (int u = 0; u < min(2, total); ++u) fetch(u);
+        float4 ds[4];
         float through = 0.f;
-        read(0);
-        for (int u = 0; u < total; ++u) {
+        int u = 0;
+        for (; u < total; ++u) {
             float4 v[4];
+            if (!tc::wait_warp(raw_done + 8 * (u & 1), u / 2, p.flag)) break;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = nx[k];
-            read(u + 1);
+            for (int k = 0; k < 4; ++k)
+                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v[k].x), "=f"(v[k].y), "=f"(v[k].z), "=f"(v[k].w)
+                             : "r"(raws + (u & 1) * kRaw + (r + 16 * k) * kTile * 4 + c * 16) : "memory");
+            mbar_arrive(raw_free + 8 * (u & 1));
             if (u & 1) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -340,22 +344,27 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                 for (int k = 0; k < 4; ++k) ds[k] = v[k];
             }
             if (u >= kUnits && !tc::wait_warp(unit_free + 8 * (u % kUnits), u / kUnits - 1, p.flag)) break;
-            const uint32_t to = units + (u % kUnits) * kUnit;
+            const uint32_t to = units + (u % kUnits) * kUnit + 8 * (c & 1);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t t[3][4];
-                split3(v[2 * k].x, v[2 * k].y, t[0][0], t[1][0], t[2][0]);
-                split3(v[2 * k].z, v[2 * k].w, t[0][1], t[1][1], t[2][1]);
-                split3(v[2 * k + 1].x, v[2 * k + 1].y, t[0][2], t[1][2], t[2][2]);
-                split3(v[2 * k + 1].z, v[2 * k + 1].w, t[0][3], t[1][3], t[2][3]);
+            for (int k = 0; k < 4; ++k) {
+                uint32_t t[3][2];
+                split3(v[k].x, v[k].y, t[0][0], t[1][0], t[2][0]);
+                split3(v[k].z, v[k].w, t[0][1], t[1][1], t[2][1]);
 #pragma unroll
                 for (int m = 0; m < 3; ++m)
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to + m * kPlane + tile_at<128>(r, 2 * c + k)), "r"(t[m][0]),
-                                 "r"(t[m][1]), "r"(t[m][2]), "r"(t[m][3])
+                    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(to + m * kPlane + tile_at<128>(r + 16 * k, c >> 1)), "r"(t[m][0]),
+                                 "r"(t[m][1])
                                  : "memory");
             }
             tc::fence_smem();
             mbar_arrive(unit_written + 8 * (u % kUnits));
+            if (i0 == 0 && u + 2 < total) {
+                if (mbar_wait(raw_free + 8 * (u & 1), (u / 2) & 1, kWaitIters))
+                    fetch(u + 2);
+                else
+                    atomicOr(p.flag, kFlagTimeout);
+            }
+            __syncwarp();
             const int head = u / (per_tile * p.tiles);
             if (u == (head + 1) * per_tile * p.tiles - 1) {     // the head's last unit
                 if (head >= 2 && !tc::wait_warp(sums_free + 8 * (head & 1), head / 2 - 1, p.flag)) break;
@@ -367,37 +376,47 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                 through = 0.f;
             }
         }
+        // left early: no copy may still be on its way when the block ends
+        if (i0 == 0)
+            for (int v = u; v < min(u + 2, total); ++v) mbar_wait(raw_done + 8 * (v & 1), (v / 2) & 1, kDrainIters);
     } else if (threadIdx.x < kScorers + kWriters + kConverters + kLoaders) {
-        const int i0 = threadIdx.x - kScorers - kWriters - kConverters, t = i0 >> 3, c = i0 & 7;   // rows t + 8 j, columns 8 c ..
-        const uint32_t place = tile_at<128>(t, c);
+        // a warp for each stage: rows t + 4 j, columns 8 c ..
+        const int mine = warp & 1, t = lane >> 3, c = lane & 7;
         auto rows = [&](uint32_t dst, const bf16* src, long long stride) {
-#pragma unroll 4
-            for (int j = 0; j < kChunk / 8; ++j) {
-                const bool on = t + 8 * j < valid;
-                cp16(dst + place + j * 1024, src + (on ? (t + 8 * j) * stride : 0) + c * 8, on);
+#pragma unroll 8
+            for (int j = 0; j < kChunk / 4; ++j) {
+                const bool on = t + 4 * j < valid;
+                cp16(dst + tile_at<128>(t + 4 * (j & 1), c) + (j >> 1) * 1024, src + (on ? (t + 4 * j) * stride : 0) + c * 8, on);
             }
         };
 #pragma unroll
         for (int b = 0; b < N / 64; ++b) {
-            rows(sb + b * kChunk * 128, p.Bm + rg.first * p.bs + group * N + b * 64, p.bs);
-            rows(sc + b * kChunk * 128, p.Cm + rg.first * p.cs + group * N + b * 64, p.cs);
+            if (mine == 0)
+                rows(sb + b * kChunk * 128, p.Bm + rg.first * p.bs + group * N + b * 64, p.bs);
+            else
+                rows(sc + b * kChunk * 128, p.Cm + rg.first * p.cs + group * N + b * 64, p.cs);
         }
         cp_commit();
-        for (int it = 0; it <= items; ++it) {
-            if (it) {   // what was issued last is there
-                cp_wait<0>();
-                tc::fence_smem();
-                if (it == 1) mbar_arrive(keys);
-                mbar_arrive(loaded + 8 * ((it - 1) & 1));
-            }
-            if (it < items) {
-                if (it >= 2 && !tc::wait_warp(emptied + 8 * (it & 1), it / 2 - 1, p.flag)) break;
-                const int h = h0 + it / p.tiles, tile = it % p.tiles;
-                const uint32_t sx = stages + (it & 1) * 2 * Sh::kX;
-                rows(sx, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs);
-                rows(sx + Sh::kX, p.dout + rg.first * os + static_cast<long long>(h) * p.P + tile * kTile, os);
-            }
+        for (int it = mine; it < items; it += 2) {
+            if (it >= 2 && !tc::wait_warp(emptied + 8 * mine, it / 2 - 1, p.flag)) break;
+            const int h = h0 + it / p.tiles, tile = it % p.tiles;
+            const uint32_t sx = stages + mine * 2 * Sh::kX;
+            rows(sx, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs);
+            rows(sx + Sh::kX, p.dout + rg.first * os + static_cast<long long>(h) * p.P + tile * kTile, os);
             cp_commit();
+            if (it == mine) {
+                cp_wait<1>();
+                tc::fence_smem();
+                mbar_arrive(keys);
+            }
+            cp_wait<0>();
+            tc::fence_smem();
+            mbar_arrive(loaded + 8 * mine);
+        }
+        if (items == 1 && mine == 1) {  // no tile for this warp
+            cp_wait<0>();
+            tc::fence_smem();
+            mbar_arrive(keys);
         }
     } else if (warp == (kBlock >> 5) - 2) {
         // a head's gates: lane l has tokens 4 l .. 4 l + 3
