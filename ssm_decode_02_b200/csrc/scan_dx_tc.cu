@@ -36,7 +36,7 @@ template <int N>
 struct Shape {
     static constexpr int kKeys = kChunk * N * 2;
     static constexpr int kX = kChunk * kTile * 2;
-    static constexpr int kSmem = 1024 + 2 * kKeys + 4 * kX + kUnits * kUnit + 2 * kRaw + 8 * 32 * (2 * 4 + 8) + 2 * kSums * 4 + 256;
+    static constexpr int kSmem = 1024 + 2 * kKeys + 4 * kX + kUnits * kUnit + 2 * kRaw + 8 * 32 * (4 + 8) + 2 * kSums * 4 + 256;
 };
 
 // v[k] of the 32 lanes added up; lane l gets the sum of v[l].
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
 
     uint8_t* smem = raw_smem + ((1024 - (smem_u32(raw_smem) & 1023)) & 1023);
     const uint32_t sb = smem_u32(smem), sc = sb + Sh::kKeys, stages = sc + Sh::kKeys, units = stages + 4 * Sh::kX, raws = units + kUnits * kUnit;
-    float* facs = reinterpret_cast<float*>(smem + 2 * Sh::kKeys + 4 * Sh::kX + kUnits * kUnit + 2 * kRaw);   // [8 warps][2][32]
-    float2* pairs = reinterpret_cast<float2*>(facs + 8 * 64);                                      // [8 warps][32]
+    float* facs = reinterpret_cast<float*>(smem + 2 * Sh::kKeys + 4 * Sh::kX + kUnits * kUnit + 2 * kRaw);   // [8 warps][32]
+    float2* pairs = reinterpret_cast<float2*>(facs + 8 * 32);                                          // [8 warps][32]
     float* sums = reinterpret_cast<float*>(pairs + 8 * 32);                                        // [2][kSums]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums + 2 * kSums);
     uint32_t bar = smem_u32(tmem_slot + 2);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
 
     if (threadIdx.x < kScorers) {
         const int half = warp >> 2;                             // columns 64 half ..
-        float* fac = facs + warp * 64;
+        float* fac = facs + warp * 32;
         float2* pair = pairs + warp * 32;
         const bool any = half * 2 + 1 >= quarter;               // some block of its columns is not before its rows
         float2 nc[2], nr = make_float2(0.f, 0.f);
@@ -134,8 +134,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
         read(0);
         bool ok = tc::wait_warp(g_done, 0, p.flag);
         for (int i = 0; i < heads && ok; ++i) {
-            float2 bc[2] = {nc[0], nc[1]};
-            const float2 br = nr;
+            const float2 bc[2] = {nc[0], nc[1]}, br = nr;
             const float dt = nd;
             read(i + 1);
             if (!(ok = tc::wait_warp(w_done, i, p.flag))) break;
@@ -144,66 +143,74 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
             tc::fence_after();
             float* out = sums + (i & 1) * kSums;
             float rows = 0.f;
-#pragma unroll
+#pragma unroll 1   // the instruction cache holds the roles' loops only if they stay small
             for (int k = 0; k < 2; ++k) {
                 const int cols = half * 2 + k;                  // this block of 32 columns
+                const float2 bk = k ? bc[1] : bc[0];
                 const uint32_t dst = tmem + kPt + cols * 16 + lanes;
                 if (cols < quarter) {                           // before every row: zero, once
                     if (i == 0) {
-                        const uint32_t z[4] = {};
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) tc::tmem_st4(dst + 4 * s, z);
+                        const uint32_t z[16] = {};
+                        tc::tmem_st16(dst, z);
                     }
                     continue;
                 }
                 const bool diagonal = cols == quarter;
                 const int meet = diagonal ? 31 : 0;
-                const float2 bm = make_float2(__shfl_sync(0xffffffffu, bc[k].x, meet), __shfl_sync(0xffffffffu, bc[k].y, meet));
-                const float first = __shfl_sync(0xffffffffu, bc[k].x, 0);
+                const float2 bm = make_float2(__shfl_sync(0xffffffffu, bk.x, meet), __shfl_sync(0xffffffffu, bk.y, meet));
+                const float first = __shfl_sync(0xffffffffu, bk.x, 0);
                 const float r = ex2_diff(bm, br);
                 const bool direct = diagonal && !(first - bm.x < 60.f);
                 __syncwarp();
-                fac[k * 32 + lane] = ex2_diff(bc[k], bm);
-                if (direct) pair[lane] = bc[k];
+                fac[lane] = ex2_diff(bk, bm);
+                if (direct) pair[lane] = bk;
                 __syncwarp();
                 float v[32], own = 0.f;
+                uint32_t o[16];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    float g[8], w[8];
-                    tc::tmem_ld8(g, tmem + kG + cols * 32 + s * 8 + lanes);
-                    tc::tmem_ld8(w, tmem + kW + cols * 32 + s * 8 + lanes);
+                for (int s = 0; s < 2; ++s) {
+                    float g[16], w[16];
+                    tc::tmem_ld16(g, tmem + kG + cols * 32 + s * 16 + lanes);
+                    tc::tmem_ld16(w, tmem + kW + cols * 32 + s * 16 + lanes);
                     tc::tmem_ld_wait();
-                    uint32_t o[4];
                     if (!direct) {
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const float4 f = reinterpret_cast<const float4*>(fac + k * 32)[s * 2 + q];
+                        for (int q = 0; q < 4; ++q) {
+                            const float4 f = reinterpret_cast<const float4*>(fac)[s * 4 + q];
                             g[4 * q] *= r * f.x;
                             g[4 * q + 1] *= r * f.y;
                             g[4 * q + 2] *= r * f.z;
                             g[4 * q + 3] *= r * f.w;
                         }
                     } else {
+#pragma unroll 1
+                        for (int q = 0; q < 16; ++q) {
+                            const float f = ex2_diff(s * 16 + q >= lane ? pair[s * 16 + q] : br, br);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) g[q] *= ex2_diff(s * 8 + q >= lane ? pair[s * 8 + q] : br, br);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int c = s * 8 + q;
-                        if (diagonal && c < lane) g[q] = 0.f;
-                        w[q] *= g[q];
-                        if (diagonal && c < lane) w[q] = 0.f;
-                        if (diagonal && c == lane) {
-                            own = w[q];
-                            w[q] = 0.f;
+                            for (int e = 0; e < 16; ++e) g[e] *= e == q ? f : 1.f;
                         }
-                        rows += w[q];
-                        v[c] = w[q] * dt;
+                    }
+                    if (diagonal) {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const int c = s * 16 + q;
+                            g[q] = c < lane ? 0.f : g[q];
+                            if (c == lane) own = w[q] * g[q];
+                            w[q] = c <= lane ? 0.f : w[q] * g[q];
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) w[q] *= g[q];
                     }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) o[q] = pack(g[2 * q], g[2 * q + 1]);
-                    tc::tmem_st4(dst + 4 * s, o);
+                    for (int q = 0; q < 16; ++q) {
+                        rows += w[q];
+                        v[s * 16 + q] = w[q] * dt;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) o[s * 8 + q] = pack(g[2 * q], g[2 * q + 1]);
                 }
+                tc::tmem_st16(dst, o);
                 out[kCol + quarter * 128 + cols * 32 + lane] = transpose_sum(v, lane);
                 if (diagonal) out[kOwn + row] = own;
             }
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
             const uint32_t sx = stages + (it & 1) * 2 * Sh::kX, sy = sx + Sh::kX;
             if (!tc::wait_warp(cd_done, it, p.flag)) break;
             tc::fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < 8; ++s) {
                 float c[8], d[8];
                 tc::tmem_ld8(c, tmem + kC + s * 8 + lanes);
@@ -290,7 +297,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
             const uint32_t sy = stages + (it & 1) * 2 * Sh::kX + Sh::kX;
             if (!tc::wait_warp(e_done, it, p.flag)) break;
             tc::fence_after();
-#pragma unroll
+#pragma unroll 2
             for (int s = 0; s < 8; ++s) {
                 float e[8];
                 uint32_t y[4];
@@ -383,7 +390,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
         // a warp for each stage: rows t + 4 j, columns 8 c ..
         const int mine = warp & 1, t = lane >> 3, c = lane & 7;
         auto rows = [&](uint32_t dst, const bf16* src, long long stride) {
-#pragma unroll 8
+#pragma unroll 4
             for (int j = 0; j < kChunk / 4; ++j) {
                 const bool on = t + 4 * j < valid;
                 cp16(dst + tile_at<128>(t + 4 * (j & 1), c) + (j >> 1) * 1024, src + (on ? (t + 4 * j) * stride : 0) + c * 8, on);
@@ -521,11 +528,12 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                     tc::fence_after();
                     const uint32_t a = (which ? sc : sb) + part * kChunk * 128, b = units + (unit % kUnits) * kUnit;
                     const uint32_t d = tmem + (which ? kE : kDd);
-#pragma unroll
+                    const uint64_t da = tc::desc(a, 16), db = tc::desc(b, 16);
+#pragma unroll 1
                     for (int m = 2; m >= 0; --m)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            tc::mma(d, tc::desc(a + ks * 32, 16), tc::desc(b + m * kPlane + ks * 2048, 16), id, part || m != 2 || ks);
+                            tc::mma(d, da + ks * 2, db + ((m * kPlane + ks * 2048) >> 4), id, part || m != 2 || ks);
                     tc::commit(unit_free + 8 * (unit % kUnits));
                 }
             if (!ok) break;
@@ -533,8 +541,9 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
             if (tile == 0 && !(ok = wait(pt_written, head))) break;
             tc::fence_after();
             const uint32_t sy = stages + (it & 1) * 2 * Sh::kX + Sh::kX;
-#pragma unroll
-            for (int ks = 0; ks < kChunk / 16; ++ks) tc::mma_ta(tmem + kC, tmem + kPt + ks * 8, tc::desc(sy + ks * 2048, 16), id, ks);
+            const uint64_t dy = tc::desc(sy, 16);
+#pragma unroll 2
+            for (int ks = 0; ks < kChunk / 16; ++ks) tc::mma_ta(tmem + kC, tmem + kPt + ks * 8, dy + ks * 128, id, ks);
             tc::commit(cd_done);
             if (tile == p.tiles - 1) tc::commit(pt_free);
         }
