@@ -137,11 +137,22 @@ rsq_status check_workspace(const char* who, size_t need, const void* ws, size_t 
     return RSQ_OK;
 }
 
-// Heads of a block of the chunk kernels: as many as share the scores' work and
-// still leave about four blocks per SM.
+// Heads of a block of the chunk kernels, one block per SM at a time: the split with
+// the fewest rounds times their length, where a block begins with work that is worth
+// about two more heads (keys, scores).
 int head_set(const Params& p) {
-    const long long all = static_cast<long long>(std::max(1, p.tokens / kChunk)) * p.H;
-    return static_cast<int>(std::max<long long>(1, std::min<long long>(p.per, all / (4 * kSms))));
+    const long long chunks = std::max(1, p.tokens / kChunk);
+    int best = p.per;
+    long long least = -1;
+    for (int set = p.per; set >= 1; --set) {
+        const long long blocks = chunks * p.G * ((p.per + set - 1) / set);
+        const long long cost = (blocks + kSms - 1) / kSms * (set * p.tiles + 2);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = set;
+        }
+    }
+    return best;
 }
 
 rsq_status done(const char* who, int err) {
