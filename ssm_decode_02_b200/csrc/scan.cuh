@@ -284,16 +284,20 @@ inline bool dx_tc_ok(const Params& p) { return (p.N == 64 || p.N == 128) && (p.P
 // The same for dB and dC.
 inline bool dk_tc_ok(const Params& p) { return p.N >= 64 && p.P >= 64; }
 
+namespace tc {
+struct Maps;
+}
+
 // Launchers (scan_forward.cu, scan_backward.cu).  Return a cudaError_t value.
 int launch_gates(const Params& p, cudaStream_t s);
-int launch_states(const Params& p, bool backward, cudaStream_t s);  // with the segments' two passes, if any
-int launch_out(const Params& p, int head_set, cudaStream_t s);
-int launch_out_tc(const Params& p, int head_set, cudaStream_t s);
+int launch_states(const Params& p, const tc::Maps& m, bool backward, cudaStream_t s);  // with the segments' two passes, if any
+int launch_out(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s);
+int launch_out_tc(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s);
 int launch_step(const Params& p, cudaStream_t s);
-int launch_states_tc(const Params& p, bool backward, const Pass& f, const Pass& b, cudaStream_t s);  // one launch
-int launch_dx_tc(const Params& p, int head_set, cudaStream_t s);
-int launch_dk_tc(const Params& p, cudaStream_t s);
-int launch_backward(const Params& p, int head_set, cudaStream_t s);
+int launch_states_tc(const Params& p, const tc::Maps& m, bool backward, const Pass& f, const Pass& b, cudaStream_t s);  // one launch
+int launch_dx_tc(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s);
+int launch_dk_tc(const Params& p, const tc::Maps& m, cudaStream_t s);
+int launch_backward(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s);
 
 }  // namespace scan
 }  // namespace rsq

@@ -4,7 +4,7 @@
 
 #include <algorithm>
 
-#include "scan.cuh"
+#include "tc.cuh"
 
 namespace rsq {
 namespace scan {
@@ -155,11 +155,49 @@ int head_set(const Params& p) {
     return best;
 }
 
+// Launches that use none of the maps leave them out (tiles of 64 columns need dk and
+// dv of 64 at least).
+int maps_for(const Params& p, bool backward, tc::Maps* m) {
+    return p.slots && p.N >= 64 && p.P >= 64 ? tc::make_maps(p, backward, m) : 0;
+}
+
 rsq_status done(const char* who, int err) {
     return err ? set_error(RSQ_E_CUDA, "%s: %s", who, cudaGetErrorString(static_cast<cudaError_t>(err))) : RSQ_OK;
 }
 
 }  // namespace
+
+int tc::make_maps(const Params& p, bool backward, Maps* m) {
+    // the driver's encoder, found once (the runtime library links no driver symbol)
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<Encode>(f);
+    }();
+    if (!encode) return cudaErrorNotSupported;
+    auto one = [&](CUtensorMap* map, const bf16* base, long long cols, long long rows, long long stride) {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+        const cuuint64_t pitch[1] = {static_cast<cuuint64_t>(stride) * 2};
+        const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<bf16*>(base), dims, pitch, box, step,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const long long hp = static_cast<long long>(p.H) * p.P, gn = static_cast<long long>(p.G) * p.N;
+    bool ok = one(&m->x, p.x, hp, p.tokens, p.xs) && one(&m->Bm, p.Bm, gn, p.tokens, p.bs) && one(&m->Cm, p.Cm, gn, p.tokens, p.cs);
+    if (backward)
+        ok = ok && one(&m->dout, p.dout, hp, p.tokens, hp);
+    else
+        ok = ok && one(&m->sh, p.sh, kTile, static_cast<long long>(p.slots) * p.H * p.tiles * p.N, kTile);
+    return ok ? 0 : cudaErrorInvalidValue;
+}
+
 }  // namespace scan
 }  // namespace rsq
 
@@ -196,9 +234,11 @@ rsq_status rsq_scan(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs, c
     p.out = static_cast<bf16*>(out);
     auto s = static_cast<cudaStream_t>(stream);
     if (steps) return done("scan", launch_step(p, s));
-    int err = p.slots ? launch_gates(p, s) : 0;
-    if (!err) err = launch_states(p, false, s);
-    if (!err && p.slots) err = launch_out(p, head_set(p), s);
+    tc::Maps m;
+    int err = maps_for(p, false, &m);
+    if (!err && p.slots) err = launch_gates(p, s);
+    if (!err) err = launch_states(p, m, false, s);
+    if (!err && p.slots) err = launch_out(p, m, head_set(p), s);
     return done("scan", err);
 }
 
@@ -233,9 +273,11 @@ rsq_status rsq_scan_backward(const rsq_scan_config* cfg, const rsq_scan_inputs* 
     p.dD = grads->dD;
     p.dstate_in = grads->dstate_in;
     auto s = static_cast<cudaStream_t>(stream);
-    int err = p.slots ? launch_gates(p, s) : 0;
-    if (!err) err = launch_states(p, true, s);
-    if (!err) err = launch_backward(p, head_set(p), s);
+    tc::Maps m;
+    int err = maps_for(p, true, &m);
+    if (!err && p.slots) err = launch_gates(p, s);
+    if (!err) err = launch_states(p, m, true, s);
+    if (!err) err = launch_backward(p, m, head_set(p), s);
     return done("scan_backward", err);
 }
 

@@ -12,7 +12,7 @@
 // (pairs on one side of t cancel in the first sum; the diagonal, which is on no
 // side, is left out of it).  They are binary32 outputs: Z comes from products of the inputs alone, and the
 // two state terms from states in three bf16 terms (split3).
-#include "scan.cuh"
+#include "tc.cuh"
 
 namespace rsq {
 namespace scan {
@@ -569,21 +569,21 @@ __global__ void __launch_bounds__(256) sums_kernel(const __grid_constant__ Param
 }
 
 template <int N>
-int backward_n(const Params& p, int head_set, cudaStream_t s) {
+int backward_n(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s) {
     int err = cudaFuncSetAttribute(dx_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, DxShape<N>::kSmem);
     if (!err) err = cudaFuncSetAttribute(dk_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, DkShape<N>::kSmem);
     if (err) return err;
     if (p.slots) {
         const dim3 grid(p.slots, p.G * ((p.per + head_set - 1) / head_set));
         if (dx_tc_ok(p)) {
-            err = launch_dx_tc(p, head_set, s);
+            err = launch_dx_tc(p, m, head_set, s);
         } else {
             dx_kernel<N><<<grid, kThreads, DxShape<N>::kSmem, s>>>(p, head_set);
             err = cudaGetLastError();
         }
         if (!err && (p.dBm || p.dCm)) {
             if (dk_tc_ok(p)) {
-                err = launch_dk_tc(p, s);
+                err = launch_dk_tc(p, m, s);
             } else {
                 dk_kernel<N><<<dim3(p.slots, p.G * (N / DkShape<N>::kW), 2), kThreads, DkShape<N>::kSmem, s>>>(p);
                 err = cudaGetLastError();
@@ -597,13 +597,13 @@ int backward_n(const Params& p, int head_set, cudaStream_t s) {
 
 }  // namespace
 
-int launch_backward(const Params& p, int head_set, cudaStream_t s) {
+int launch_backward(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s) {
     switch (p.N) {
-        case 16: return backward_n<16>(p, head_set, s);
-        case 32: return backward_n<32>(p, head_set, s);
-        case 64: return backward_n<64>(p, head_set, s);
-        case 128: return backward_n<128>(p, head_set, s);
-        default: return backward_n<256>(p, head_set, s);
+        case 16: return backward_n<16>(p, m, head_set, s);
+        case 32: return backward_n<32>(p, m, head_set, s);
+        case 64: return backward_n<64>(p, m, head_set, s);
+        case 128: return backward_n<128>(p, m, head_set, s);
+        default: return backward_n<256>(p, m, head_set, s);
     }
 }
 

@@ -26,7 +26,7 @@ constexpr int kW = 0, kM = 256, kT = 384;       // tensor memory: two of dout x^
 // M and the keys come where the stages were
 constexpr int kSmem = 1024 + kStages * 2 * kX + kUnits * kUnit + kRaws * kRaw + 8 * 32 * (2 * 4 + 16) + 384;
 
-__global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ tc::Maps maps) {
     extern __shared__ uint8_t raw_smem[];
     const Range rg = slot_range(p, blockIdx.x, kChunk);
     if (!rg.valid) return;
@@ -52,14 +52,14 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
                    m_written = next_bar(1), f_done = next_bar(1), heads_done = next_bar(1), raw_done = next_bar(kRaws), raw_free = next_bar(kRaws);
     if (warp == 0) tc::tmem_alloc(smem_u32(tmem_slot), 512);
     if (threadIdx.x == 0) {
-        mbar_init(keys, 64);
+        mbar_init(keys, 2);
         mbar_init(t_done, 1);
         mbar_init(t_free, kSummers);
         mbar_init(m_written, kScorers);
         mbar_init(f_done, 1);
         mbar_init(heads_done, 1);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(loaded + 8 * i, 32);
+            mbar_init(loaded + 8 * i, 1);
             mbar_init(emptied + 8 * i, 1);
         }
         for (int i = 0; i < kRaws; ++i) {
@@ -268,36 +268,58 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
         if (i0 == 0)
             for (int v = u; v < min(u + kRaws, total); ++v) mbar_wait(raw_done + 8 * (v % kRaws), (v / kRaws) & 1, kDrainIters);
     } else if (threadIdx.x < kScorers + kSummers + kConverters + kLoaders) {
-        // a warp for each stage: rows t + 4 j, columns 8 c ..
+        // a warp for each stage.  A whole chunk's tiles come in boxes; the last rows of a
+        // sequence, which the next one's may follow, row by row with zeros behind them.
         const int mine = warp - (kScorers + kSummers + kConverters) / 32, t = lane >> 3, c = lane & 7;
+        const bool whole = valid == kChunk;
         auto rows = [&](uint32_t dst, const bf16* src, long long stride) {
-#pragma unroll 8
+#pragma unroll 4
             for (int j = 0; j < kChunk / 4; ++j) {
                 const bool on = t + 4 * j < valid;
                 cp16(dst + tile_at<128>(t + 4 * (j & 1), c) + (j >> 1) * 1024, src + (on ? (t + 4 * j) * stride : 0) + c * 8, on);
             }
         };
+        auto announce = [&](uint32_t b) {
+            cp_commit();
+            cp_wait<0>();
+            tc::fence_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b);
+        };
         bool ok = true;
         for (int it = mine; it < items; it += kStages) {
             if (it >= kStages && !(ok = tc::wait_warp(emptied + 8 * mine, it / kStages - 1, p.flag))) break;
             const int h = h0 + it / p.tiles, tile = it % p.tiles;
-            const uint32_t sx = stages + mine * 2 * kX;
-            rows(sx, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs);
-            rows(sx + kX, p.dout + rg.first * os + static_cast<long long>(h) * p.P + tile * kTile, os);
-            cp_commit();
-            cp_wait<0>();
-            tc::fence_smem();
-            mbar_arrive(loaded + 8 * mine);
+            const uint32_t sx = stages + mine * 2 * kX, b = loaded + 8 * mine;
+            if (whole) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(b, 2 * kX);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        tc::box(sx + k * tc::kBox, &maps.x, h * p.P + tile * kTile, rg.first + k * 64, b);
+                        tc::box(sx + kX + k * tc::kBox, &maps.dout, h * p.P + tile * kTile, rg.first + k * 64, b);
+                    }
+                }
+                __syncwarp();
+            } else {
+                rows(sx, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs);
+                rows(sx + kX, p.dout + rg.first * os + static_cast<long long>(h) * p.P + tile * kTile, os);
+                announce(b);
+            }
         }
         if (mine < 2 && ok && tc::wait_warp(heads_done, 0, p.flag)) {
-            if (mine == 0)
-                rows(sk, p.Bm + rg.first * p.bs + group * p.N + n0, p.bs);
-            else
-                rows(sk + kX, p.Cm + rg.first * p.cs + group * p.N + n0, p.cs);
-            cp_commit();
-            cp_wait<0>();
-            tc::fence_smem();
-            mbar_arrive(keys);
+            if (whole) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(keys, kX);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        tc::box(sk + mine * kX + k * tc::kBox, mine ? &maps.Cm : &maps.Bm, group * p.N + n0, rg.first + k * 64, keys);
+                }
+                __syncwarp();
+            } else {
+                rows(sk + mine * kX, (mine ? p.Cm + rg.first * p.cs : p.Bm + rg.first * p.bs) + group * p.N + n0, mine ? p.cs : p.bs);
+                announce(keys);
+            }
         }
     } else if (lane == 0) {
         auto wait = [&](uint32_t b, int phase) { return mbar_wait(b, phase & 1, kWaitIters); };
@@ -340,7 +362,12 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
                 tc::mma(tmem + kT + 64, tc::desc(sm + ks * 2048, kX), tc::desc(sk + kX + ks * 2048, 16), id_b, ks);
             tc::commit(f_done);
         }
-        if (!ok) atomicOr(p.flag, kFlagTimeout);
+        if (!ok) {  // left early: no box may still be on its way when the block ends
+            atomicOr(p.flag, kFlagTimeout);
+            for (int i = 0; i < kStages; ++i)
+                for (int k = 0; k < 2; ++k) mbar_wait(loaded + 8 * i, k, kDrainIters);
+            mbar_wait(keys, 0, kDrainIters);
+        }
     }
     tc::fence_before();
     __syncthreads();
@@ -349,10 +376,10 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
 
 }  // namespace
 
-int launch_dk_tc(const Params& p, cudaStream_t s) {
+int launch_dk_tc(const Params& p, const tc::Maps& m, cudaStream_t s) {
     const int err = cudaFuncSetAttribute(dk_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (err) return err;
-    dk_tc_kernel<<<dim3(p.slots, p.G * (p.N / 64)), kBlock, kSmem, s>>>(p);
+    dk_tc_kernel<<<dim3(p.slots, p.G * (p.N / 64)), kBlock, kSmem, s>>>(p, m);
     return cudaGetLastError();
 }
 

@@ -54,7 +54,8 @@ __device__ __forceinline__ float transpose_sum(float (&v)[32], int lane) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant__ Params p, int head_set) {
+__global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ tc::Maps maps,
+                                                           int head_set) {
     using Sh = Shape<N>;
     extern __shared__ uint8_t raw_smem[];
     const Range rg = slot_range(p, blockIdx.x, kChunk);
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                    sums_done = next_bar(2), sums_free = next_bar(2), raw_done = next_bar(2), raw_free = next_bar(2);
     if (warp == 0) tc::tmem_alloc(smem_u32(tmem_slot), 512);
     if (threadIdx.x == 0) {
-        mbar_init(keys, kLoaders);
+        mbar_init(keys, 2);
         for (uint32_t b : {g_done, w_done, pt_free, cd_done, e_done}) mbar_init(b, 1);
         for (uint32_t b : {w_free, pt_written}) mbar_init(b, kScorers);
         for (uint32_t b : {cd_free, e_free}) mbar_init(b, 128);
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
             mbar_init(unit_free + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(loaded + 8 * i, 32);
+            mbar_init(loaded + 8 * i, 1);
             mbar_init(raw_done + 8 * i, 1);
             mbar_init(raw_free + 8 * i, kConverters);
             mbar_init(emptied + 8 * i, kWriters);
@@ -278,6 +279,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                     if (r < valid) *reinterpret_cast<uint4*>(out + r * os + (lane & 7) * 8) = v;
                 }
             }
+            tc::fence_smem();   // boxes overwrite what was written here
             mbar_arrive(emptied + 8 * (it & 1));
             if (tile == p.tiles - 1) {
                 if (head >= 2 && !tc::wait_warp(sums_free + 8 * (head & 1), head / 2 - 1, p.flag)) break;
@@ -387,8 +389,10 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
         if (i0 == 0)
             for (int v = u; v < min(u + 2, total); ++v) mbar_wait(raw_done + 8 * (v & 1), (v / 2) & 1, kDrainIters);
     } else if (threadIdx.x < kScorers + kWriters + kConverters + kLoaders) {
-        // a warp for each stage: rows t + 4 j, columns 8 c ..
+        // a warp for each stage.  A whole chunk's tiles come in boxes; the last rows of a
+        // sequence, which the next one's may follow, row by row with zeros behind them.
         const int mine = warp & 1, t = lane >> 3, c = lane & 7;
+        const bool whole = valid == kChunk;
         auto rows = [&](uint32_t dst, const bf16* src, long long stride) {
 #pragma unroll 4
             for (int j = 0; j < kChunk / 4; ++j) {
@@ -396,34 +400,49 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                 cp16(dst + tile_at<128>(t + 4 * (j & 1), c) + (j >> 1) * 1024, src + (on ? (t + 4 * j) * stride : 0) + c * 8, on);
             }
         };
+        auto announce = [&](uint32_t b) {
+            cp_commit();
+            cp_wait<0>();
+            tc::fence_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b);
+        };
+        const uint32_t sk = mine ? sc : sb;
+        if (whole) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(keys, Sh::kKeys);
 #pragma unroll
-        for (int b = 0; b < N / 64; ++b) {
-            if (mine == 0)
-                rows(sb + b * kChunk * 128, p.Bm + rg.first * p.bs + group * N + b * 64, p.bs);
-            else
-                rows(sc + b * kChunk * 128, p.Cm + rg.first * p.cs + group * N + b * 64, p.cs);
+                for (int b = 0; b < N / 64; ++b)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        tc::box(sk + b * kChunk * 128 + k * tc::kBox, mine ? &maps.Cm : &maps.Bm, group * N + b * 64, rg.first + k * 64, keys);
+            }
+            __syncwarp();
+        } else {
+#pragma unroll 1
+            for (int b = 0; b < N / 64; ++b)
+                rows(sk + b * kChunk * 128, (mine ? p.Cm + rg.first * p.cs : p.Bm + rg.first * p.bs) + group * N + b * 64, mine ? p.cs : p.bs);
+            announce(keys);
         }
-        cp_commit();
         for (int it = mine; it < items; it += 2) {
             if (it >= 2 && !tc::wait_warp(emptied + 8 * mine, it / 2 - 1, p.flag)) break;
             const int h = h0 + it / p.tiles, tile = it % p.tiles;
-            const uint32_t sx = stages + mine * 2 * Sh::kX;
-            rows(sx, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs);
-            rows(sx + Sh::kX, p.dout + rg.first * os + static_cast<long long>(h) * p.P + tile * kTile, os);
-            cp_commit();
-            if (it == mine) {
-                cp_wait<1>();
-                tc::fence_smem();
-                mbar_arrive(keys);
+            const uint32_t sx = stages + mine * 2 * Sh::kX, b = loaded + 8 * mine;
+            if (whole) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(b, 2 * Sh::kX);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        tc::box(sx + k * tc::kBox, &maps.x, h * p.P + tile * kTile, rg.first + k * 64, b);
+                        tc::box(sx + Sh::kX + k * tc::kBox, &maps.dout, h * p.P + tile * kTile, rg.first + k * 64, b);
+                    }
+                }
+                __syncwarp();
+            } else {
+                rows(sx, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs);
+                rows(sx + Sh::kX, p.dout + rg.first * os + static_cast<long long>(h) * p.P + tile * kTile, os);
+                announce(b);
             }
-            cp_wait<0>();
-            tc::fence_smem();
-            mbar_arrive(loaded + 8 * mine);
-        }
-        if (items == 1 && mine == 1) {  // no tile for this warp
-            cp_wait<0>();
-            tc::fence_smem();
-            mbar_arrive(keys);
         }
     } else if (warp == (kBlock >> 5) - 2) {
         // a head's gates: lane l has tokens 4 l .. 4 l + 3
@@ -547,7 +566,12 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
             tc::commit(cd_done);
             if (tile == p.tiles - 1) tc::commit(pt_free);
         }
-        if (!ok) atomicOr(p.flag, kFlagTimeout);
+        if (!ok) {  // left early: no box may still be on its way when the block ends
+            atomicOr(p.flag, kFlagTimeout);
+            for (int i = 0; i < 2; ++i)
+                for (int k = 0; k < 2; ++k) mbar_wait(loaded + 8 * i, k, kDrainIters);
+            mbar_wait(keys, 0, kDrainIters);
+        }
     }
     tc::fence_before();
     __syncthreads();
@@ -555,18 +579,18 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
 }
 
 template <int N>
-int run(const Params& p, int head_set, cudaStream_t s) {
+int run(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s) {
     const int err = cudaFuncSetAttribute(dx_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<N>::kSmem);
     if (err) return err;
     const dim3 grid(p.slots, p.G * ((p.per + head_set - 1) / head_set));
-    dx_tc_kernel<N><<<grid, kBlock, Shape<N>::kSmem, s>>>(p, head_set);
+    dx_tc_kernel<N><<<grid, kBlock, Shape<N>::kSmem, s>>>(p, m, head_set);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-int launch_dx_tc(const Params& p, int head_set, cudaStream_t s) {
-    return p.N == 64 ? run<64>(p, head_set, s) : run<128>(p, head_set, s);
+int launch_dx_tc(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s) {
+    return p.N == 64 ? run<64>(p, m, head_set, s) : run<128>(p, m, head_set, s);
 }
 
 }  // namespace scan

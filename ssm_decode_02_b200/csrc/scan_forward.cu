@@ -1,6 +1,6 @@
 // scan_forward.cu -- the scan's gates, states and outputs (sm_100a); the backward
 // pass uses the first two as well.
-#include "scan.cuh"
+#include "tc.cuh"
 
 namespace rsq {
 namespace scan {
@@ -549,9 +549,9 @@ int allow_smem(F* f, int bytes) {
 }
 
 template <int N>
-int states_n(const Params& p, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
+int states_n(const Params& p, const tc::Maps& m, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
     using Sh = StateShape<N>;
-    if (N >= 64 && states_tc_ok(p)) return launch_states_tc(p, backward, f, b, s);
+    if (N >= 64 && states_tc_ok(p)) return launch_states_tc(p, m, backward, f, b, s);
     const dim3 grid(p.seg_chunks ? p.seg_slots : p.n, p.H * p.tiles, backward ? 2 : 1);
     auto* k = backward ? states_kernel<N, true> : states_kernel<N, false>;
     const int err = allow_smem(k, Sh::kSmem);
@@ -560,13 +560,13 @@ int states_n(const Params& p, bool backward, const Pass& f, const Pass& b, cudaS
     return cudaGetLastError();
 }
 
-int states_pass(const Params& p, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
+int states_pass(const Params& p, const tc::Maps& m, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
     switch (p.N) {
-        case 16: return states_n<16>(p, backward, f, b, s);
-        case 32: return states_n<32>(p, backward, f, b, s);
-        case 64: return states_n<64>(p, backward, f, b, s);
-        case 128: return states_n<128>(p, backward, f, b, s);
-        default: return states_n<256>(p, backward, f, b, s);
+        case 16: return states_n<16>(p, m, backward, f, b, s);
+        case 32: return states_n<32>(p, m, backward, f, b, s);
+        case 64: return states_n<64>(p, m, backward, f, b, s);
+        case 128: return states_n<128>(p, m, backward, f, b, s);
+        default: return states_n<256>(p, m, backward, f, b, s);
     }
 }
 
@@ -587,18 +587,18 @@ int launch_gates(const Params& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-int launch_states(const Params& p, bool backward, cudaStream_t s) {
+int launch_states(const Params& p, const tc::Maps& m, bool backward, cudaStream_t s) {
     const Pass f{p.Bm, p.x, p.bs, p.xs, p.state_in, p.state_out, 0, 0};
     const Pass b{backward ? p.Cm : nullptr, p.dout, p.cs, static_cast<long long>(p.H) * p.P, p.dstate_out, p.dstate_in, 1, 0};
     if (p.seg_chunks) {
         Pass lf = f, lb = b;
         lf.local = lb.local = 1;
-        int err = states_pass(p, backward, lf, lb, s);
+        int err = states_pass(p, m, backward, lf, lb, s);
         if (err) return err;
         segments_kernel<<<dim3((p.N * p.P / 4 + kThreads - 1) / kThreads, p.H, 2 * p.n), kThreads, 0, s>>>(p, f, b);
         if ((err = cudaGetLastError())) return err;
     }
-    return states_pass(p, backward, f, b, s);
+    return states_pass(p, m, backward, f, b, s);
 }
 
 int launch_step(const Params& p, cudaStream_t s) {
@@ -613,8 +613,8 @@ int launch_step(const Params& p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-int launch_out(const Params& p, int head_set, cudaStream_t s) {
-    if (out_tc_ok(p)) return launch_out_tc(p, head_set, s);
+int launch_out(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s) {
+    if (out_tc_ok(p)) return launch_out_tc(p, m, head_set, s);
     switch (p.N) {
         case 16: return out_n<16>(p, head_set, s);
         case 32: return out_n<32>(p, head_set, s);

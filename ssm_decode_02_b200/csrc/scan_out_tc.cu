@@ -43,7 +43,8 @@ struct Shape {
 };
 
 template <int N>
-__global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant__ Params p, int head_set) {
+__global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ tc::Maps maps,
+                                                            int head_set) {
     using Sh = Shape<N>;
     extern __shared__ uint8_t raw_smem[];
     const Range rg = slot_range(p, blockIdx.x, kChunk);
@@ -65,10 +66,10 @@ __global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant
                    left_free = left + 16, tile_done = left_free + 16, tile_free = tile_done + 16;
     if (warp == 0) tc::tmem_alloc(smem_u32(tmem_slot), kTmem);
     if (threadIdx.x == 0) {
-        mbar_init(keys, kLoaders);
+        mbar_init(keys, 1);
         mbar_init(scores, 1);
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(loaded + 8 * i, kLoaders);
+            mbar_init(loaded + 8 * i, 1);
             mbar_init(emptied + 8 * i, 128);
         }
         for (int i = 0; i < 2; ++i) {
@@ -222,41 +223,69 @@ __global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant
                              : "r"(st + tile_at<128>(r, lane & 7)) : "memory");
                 if (r < valid) *reinterpret_cast<uint4*>(out + r * os + (lane & 7) * 8) = v;
             }
+            tc::fence_smem();   // boxes overwrite what was written here
             mbar_arrive(emptied + 8 * (it % kStages));
         }
     } else if (threadIdx.x < kScorers + kWriters + kLoaders) {
-        const int i0 = threadIdx.x - kScorers - kWriters, t = i0 >> 3, c = i0 & 7;   // rows t + 8 j, columns 8 c ..
-        const uint32_t place = tile_at<128>(t, c);
+        // a whole chunk's tiles come in boxes; the last rows of a sequence, which the next
+        // one's may follow, row by row with zeros behind them.  Every other tile for a warp.
+        const int mine = warp & 1, t = lane >> 3, c = lane & 7;
+        const bool whole = valid == kChunk;
         auto rows = [&](uint32_t dst, const bf16* src, long long stride, int n, int on_rows) {
 #pragma unroll 4
-            for (int j = 0; j < n; ++j) {
-                const bool on = t + 8 * j < on_rows;
-                cp16(dst + place + j * 1024, src + (on ? (t + 8 * j) * stride : 0) + c * 8, on);
+            for (int j = 0; j < n / 4; ++j) {
+                const bool on = t + 4 * j < on_rows;
+                cp16(dst + tile_at<128>(t + 4 * (j & 1), c) + (j >> 1) * 1024, src + (on ? (t + 4 * j) * stride : 0) + c * 8, on);
             }
         };
-#pragma unroll
-        for (int b = 0; b < N / 64; ++b) {
-            rows(sc + b * kChunk * 128, p.Cm + rg.first * p.cs + group * N + b * 64, p.cs, kChunk / 8, valid);
-            rows(sb + b * kChunk * 128, p.Bm + rg.first * p.bs + group * N + b * 64, p.bs, kChunk / 8, valid);
-        }
-        cp_commit();
-        // a stage is announced before the wait for room for the next but one: announcing it
-        // later would tie every tile to the writers of the tile two before it
-        for (int it = 0; it <= items + 1; ++it) {
-            cp_wait<1>();
-            tc::fence_smem();
-            if (it) mbar_arrive(it == 1 ? keys : loaded + 8 * ((it - 2) % kStages));
-            if (it < items) {
-                const int h = h0 + it / p.tiles, tile = it % p.tiles;
-                const uint32_t st = stages + (it % kStages) * Sh::kStage;
-                if (it >= kStages && !tc::wait_warp(emptied + 8 * (it % kStages), it / kStages - 1, p.flag)) break;
-                rows(st, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs, kChunk / 8, valid);
-                const long long cell = (static_cast<long long>(blockIdx.x) * p.H + h) * p.tiles + tile;
-                rows(st + Sh::kX, p.sh + cell * N * kTile, kTile, N / 8, N);
-            }
+        auto announce = [&](uint32_t b) {
             cp_commit();
+            cp_wait<0>();
+            tc::fence_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b);
+        };
+        if (mine == 0) {
+            if (whole) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(keys, 2 * Sh::kKeys);
+#pragma unroll
+                    for (int b = 0; b < N / 64; ++b)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            tc::box(sc + b * kChunk * 128 + k * tc::kBox, &maps.Cm, group * N + b * 64, rg.first + k * 64, keys);
+                            tc::box(sb + b * kChunk * 128 + k * tc::kBox, &maps.Bm, group * N + b * 64, rg.first + k * 64, keys);
+                        }
+                }
+            } else {
+#pragma unroll 1
+                for (int b = 0; b < N / 64; ++b) {
+                    rows(sc + b * kChunk * 128, p.Cm + rg.first * p.cs + group * N + b * 64, p.cs, kChunk, valid);
+                    rows(sb + b * kChunk * 128, p.Bm + rg.first * p.bs + group * N + b * 64, p.bs, kChunk, valid);
+                }
+                announce(keys);
+            }
         }
-        cp_wait<0>();
+        for (int it = mine; it < items; it += 2) {
+            const int h = h0 + it / p.tiles, tile = it % p.tiles;
+            const uint32_t st = stages + (it % kStages) * Sh::kStage, b = loaded + 8 * (it % kStages);
+            if (it >= kStages && !tc::wait_warp(emptied + 8 * (it % kStages), it / kStages - 1, p.flag)) break;
+            const long long cell = (static_cast<long long>(blockIdx.x) * p.H + h) * p.tiles + tile;
+            if (whole) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(b, Sh::kStage);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) tc::box(st + k * tc::kBox, &maps.x, h * p.P + tile * kTile, rg.first + k * 64, b);
+#pragma unroll
+                    for (int k = 0; k < N / 64; ++k) tc::box(st + Sh::kX + k * tc::kBox, &maps.sh, 0, static_cast<int>(cell * N) + k * 64, b);
+                }
+                __syncwarp();
+            } else {
+                rows(st, p.x + rg.first * p.xs + static_cast<long long>(h) * p.P + tile * kTile, p.xs, kChunk, valid);
+                rows(st + Sh::kX, p.sh + cell * N * kTile, kTile, N, N);
+                announce(b);
+            }
+        }
     } else if (lane == 0) {
         bool ok = mbar_wait(keys, 0, kWaitIters);
         if (ok) {
@@ -287,7 +316,12 @@ __global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant
             tc::commit(tile_done + 8 * (it & 1));
             if (tile == p.tiles - 1) tc::commit(left_free + 8 * buf);
         }
-        if (!ok) atomicOr(p.flag, kFlagTimeout);
+        if (!ok) {  // left early: no box may still be on its way when the block ends
+            atomicOr(p.flag, kFlagTimeout);
+            for (int i = 0; i < kStages; ++i)
+                for (int k = 0; k < 2; ++k) mbar_wait(loaded + 8 * i, k, kDrainIters);
+            mbar_wait(keys, 0, kDrainIters);
+        }
     }
     tc::fence_before();
     __syncthreads();
@@ -295,18 +329,18 @@ __global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant
 }
 
 template <int N>
-int run(const Params& p, int head_set, cudaStream_t s) {
+int run(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s) {
     const int err = cudaFuncSetAttribute(out_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<N>::kSmem);
     if (err) return err;
     const dim3 grid(p.slots, p.G * ((p.per + head_set - 1) / head_set));
-    out_tc_kernel<N><<<grid, kBlock, Shape<N>::kSmem, s>>>(p, head_set);
+    out_tc_kernel<N><<<grid, kBlock, Shape<N>::kSmem, s>>>(p, m, head_set);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-int launch_out_tc(const Params& p, int head_set, cudaStream_t s) {
-    return p.N == 64 ? run<64>(p, head_set, s) : run<128>(p, head_set, s);
+int launch_out_tc(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s) {
+    return p.N == 64 ? run<64>(p, m, head_set, s) : run<128>(p, m, head_set, s);
 }
 
 }  // namespace scan

@@ -7,7 +7,7 @@
 // of the weighted values, 128 x tokens in three bf16 terms (split3), with the keys,
 // tokens x N, is a tcgen05 product into one of two tensor-memory tiles.  Three kinds
 // of warps, which meet at mbarriers only:
-//   8 converters  copy keys and values of half a chunk ahead (cp.async, four stages),
+//   8 converters  have keys and values of half a chunk copied ahead (four stages),
 //                 weight the values and write their terms (two buffers);
 //   8 updaters    hold the state, a thread half a column of N binary32; they store it
 //                 as the state before the chunk and take in the chunk's tile while the
@@ -30,12 +30,13 @@ struct Shape {
     static constexpr int kValues = kHalf * kCols * 2;
     static constexpr int kStage = kKeys + kValues;
     static constexpr int kTerms = 3 * kValues;
-    static constexpr int kSmem = 1024 + kStages * kStage + 2 * kTerms + 128;
+    static constexpr int kSmem = 1024 + kStages * kStage + 2 * kTerms + 192;
 };
 
 template <int N, bool F32>
 __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ Pass fwd,
-                                                               const __grid_constant__ Pass bwd) {
+                                                               const __grid_constant__ Pass bwd,
+                                                               const __grid_constant__ tc::Maps maps) {
     using Sh = Shape<N>;
     extern __shared__ uint8_t raw_smem[];
     const Pass& ps = blockIdx.z ? bwd : fwd;
@@ -67,7 +68,8 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kStages * Sh::kStage + 2 * Sh::kTerms);
     // barriers, two of each: terms and keys written; their products done; a tile
     // complete; a tile taken in
-    const uint32_t written = smem_u32(tmem_slot + 2), done = written + 16, full = done + 16, taken = full + 16;
+    const uint32_t written = smem_u32(tmem_slot + 2), done = written + 16, full = done + 16, taken = full + 16,
+                   arrived = taken + 16;  // and a stage's boxes, four
     if (warp == 0) tc::tmem_alloc(smem_u32(tmem_slot), 2 * N);
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -77,6 +79,7 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
             mbar_init(full + 8 * i, 1);
             mbar_init(taken + 8 * i, kUpdaters);
         }
+        for (int i = 0; i < kStages; ++i) mbar_init(arrived + 8 * i, 1);
         fence_mbar_init();
     }
     tc::fence_before();
@@ -91,12 +94,28 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
         const bf16* kp = ps.k + static_cast<long long>(group) * p.N + row0 + c * 8;
         const bf16* vp = ps.v + c0 + c * 8;
         const int h1 = heads - 1;                   // head of columns 64..127, from h0
+        // a step of 64 rows comes in boxes that one thread asks for; the last rows of a
+        // sequence, which the next one's may follow, chunk by chunk with zeros behind them
+        const CUtensorMap *kmap = ps.rev ? &maps.Cm : &maps.Bm, *vmap = ps.rev ? &maps.dout : &maps.x;
         auto load = [&](int s) {
             if (s < steps) {
                 const int row = chunk_of(s) * kChunk + (s & 1) * kHalf + t;
                 const uint32_t st = base + (s % kStages) * Sh::kStage + place;
+                const bool whole = row - t + kHalf <= len;
+                if (threadIdx.x == 0) {
+                    const uint32_t b = arrived + 8 * (s % kStages), to = base + (s % kStages) * Sh::kStage;
+                    if (whole) {
+                        mbar_arrive_expect_tx(b, Sh::kStage);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                        for (int k = 0; k < N / 64; ++k) tc::box(to + k * 8192, kmap, group * p.N + row0 + k * 64, lo + row, b);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) tc::box(to + Sh::kKeys + k * 8192, vmap, c0 + k * 64, lo + row, b);
+                    } else {
+                        mbar_arrive(b);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 2 && !whole; ++j) {
                     const bool on = row + 32 * j < len;
                     const long long at = lo + (on ? row + 32 * j : 0);
                     const bf16 *ksrc = kp + at * ps.ks, *vsrc = vp + at * ps.vs;
@@ -127,7 +146,8 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
         load(0);
         load(1);
         read_gates(0);
-        for (int s = 0; s < steps; ++s) {
+        int s = 0;
+        for (; s < steps; ++s) {
             float w[2][2];
 #pragma unroll
             for (int b = 0; b < 2; ++b)
@@ -135,6 +155,7 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
                 for (int j = 0; j < 2; ++j) w[b][j] = ps.rev ? ex2(gb[b][j].x + gb[b][j].y) : ex2_diff(ge[b], gb[b][j]) * gd[b][j];
             read_gates(s + 1);
             cp_wait<1>();
+            if (!tc::wait_warp(arrived + 8 * (s % kStages), s / kStages, p.flag)) break;
             // the products of step s - 2 are done with the terms' buffer and with the stage loaded below
             if (s >= 2 && !tc::wait_warp(done + 8 * (s & 1), s / 2 - 1, p.flag)) break;
             const uint32_t st = base + (s % kStages) * Sh::kStage + Sh::kKeys + place, tb = terms + (s & 1) * Sh::kTerms + place;
@@ -159,6 +180,9 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
             load(s + 2);
         }
         cp_wait<0>();
+        // left early: no box may still be on its way when the block ends
+        if (threadIdx.x == 0)
+            for (int k = s; k < min(s + 2, steps); ++k) mbar_wait(arrived + 8 * (k % kStages), (k / kStages) & 1, kDrainIters);
     } else if (threadIdx.x < kConverters + kUpdaters) {
         // value column m (the tensor-memory lane), state rows n0 .. n0 + R - 1 of the block's
         constexpr int R = N / 2;
@@ -246,19 +270,19 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
 }
 
 template <int N>
-int run(const Params& p, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
+int run(const Params& p, const tc::Maps& m, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
     auto* k = backward ? states_tc_kernel<N, true> : states_tc_kernel<N, false>;
     const int err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<N>::kSmem);
     if (err) return err;
     const dim3 grid(p.seg_chunks ? p.seg_slots : p.n, p.H * p.P / kCols * (p.N / N), backward ? 2 : 1);
-    k<<<grid, kBlock, Shape<N>::kSmem, s>>>(p, f, b);
+    k<<<grid, kBlock, Shape<N>::kSmem, s>>>(p, f, b, m);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-int launch_states_tc(const Params& p, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
-    return p.N == 64 ? run<64>(p, backward, f, b, s) : run<128>(p, backward, f, b, s);
+int launch_states_tc(const Params& p, const tc::Maps& m, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
+    return p.N == 64 ? run<64>(p, m, backward, f, b, s) : run<128>(p, m, backward, f, b, s);
 }
 
 }  // namespace scan

@@ -8,11 +8,28 @@
 //   mn-major: a row is one k, its 64 columns are 64 m (or n)
 #pragma once
 
+#include <cuda.h>
+
 #include "scan.cuh"
 
 namespace rsq {
 namespace scan {
 namespace tc {
+
+// ---- tiled copies ----------------------------------------------------------
+// Boxes of 64 columns by 64 rows of the token arrays and of the bf16 states, written
+// in the tiles' order (128-byte swizzle).  No multicast.
+struct Maps {
+    CUtensorMap x, Bm, Cm, dout, sh;
+};
+int make_maps(const Params& p, bool backward, Maps* m);  // scan_api.cu; a cudaError_t value
+
+__device__ __forceinline__ void box(uint32_t dst, const CUtensorMap* map, int col, int row, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"(map), "r"(col), "r"(row), "r"(bar)
+                 : "memory");
+}
+constexpr uint32_t kBox = 64 * 128;  // bytes
 
 // ---- tensor memory ---------------------------------------------------------
 // Called by one whole warp; the base address is written to shared memory.
