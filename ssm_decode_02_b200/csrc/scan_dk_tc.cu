@@ -321,49 +321,63 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
                 announce(keys);
             }
         }
-    } else if (lane == 0) {
-        auto wait = [&](uint32_t b, int phase) { return mbar_wait(b, phase & 1, kWaitIters); };
+    } else {
+        auto wait = [&](uint32_t b, int phase) { return tc::wait_warp(b, phase, p.flag); };
         bool ok = true;
         constexpr uint32_t id_w = tc::idesc(kChunk, false, false), id_t = tc::idesc(64, false, false);
+        const uint64_t stage0 = tc::desc(stages, 16), unit0 = tc::desc(units, 16);
+        int head = 0, tile = 0;
         for (int it = 0; it < items && ok; ++it) {
-            const int head = it / p.tiles, tile = it - head * p.tiles;
             if (!(ok = wait(loaded + 8 * (it % kStages), it / kStages))) break;
             if (tile == 0 && head >= 2 && !(ok = wait(w_free + 8 * (head & 1), head / 2 - 1))) break;
             tc::fence_after();
-            const uint32_t sx = stages + (it % kStages) * 2 * kX, sy = sx + kX, w = tmem + kW + (head & 1) * 128;
+            const uint64_t xd = stage0 + (it % kStages) * (2 * kX >> 4), yd = xd + (kX >> 4);
+            const uint32_t w = tmem + kW + (head & 1) * 128;
+            const bool last = tile == p.tiles - 1;
+            if (tc::elect()) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) tc::mma(w, tc::desc(sy + ks * 32, 16), tc::desc(sx + ks * 32, 16), id_w, tile || ks);
-            if (tile == p.tiles - 1) tc::commit(w_done + 8 * (head & 1));
+                for (int ks = 0; ks < 4; ++ks) tc::mma(w, yd + ks * 2, xd + ks * 2, id_w, ks || tile);
+                if (last) tc::commit(w_done + 8 * (head & 1));
+            }
+            __syncwarp();
             if (tile == 0 && head && !(ok = wait(t_free, head - 1))) break;
-#pragma unroll
-            for (int which = 0; which < 2; ++which) {
+            for (int which = 0; which < 2 && ok; ++which) {
                 const int u = 2 * it + which;
                 if (!(ok = wait(unit_written + 8 * (u % kUnits), u / kUnits))) break;
                 tc::fence_after();
+                const uint64_t a = which ? xd : yd, b = unit0 + (u % kUnits) * (kUnit >> 4);
+                if (tc::elect()) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    tc::mma(tmem + kT + which * 64, tc::desc((which ? sx : sy) + ks * 32, 16),
-                            tc::desc(units + (u % kUnits) * kUnit + ks * 32, 16), id_t, tile || ks);
-                tc::commit(unit_free + 8 * (u % kUnits));
+                    for (int ks = 0; ks < 4; ++ks) tc::mma(tmem + kT + which * 64, a + ks * 2, b + ks * 2, id_t, ks || tile);
+                    tc::commit(unit_free + 8 * (u % kUnits));
+                }
+                __syncwarp();
             }
             if (!ok) break;
-            tc::commit(emptied + 8 * (it % kStages));
-            if (tile == p.tiles - 1) tc::commit(t_done);
+            if (tc::elect()) {
+                tc::commit(emptied + 8 * (it % kStages));
+                if (last) tc::commit(t_done);
+            }
+            __syncwarp();
+            tile = last ? 0 : tile + 1;
+            head += last;
         }
-        if (ok) tc::commit(heads_done);
+        if (ok && tc::elect()) tc::commit(heads_done);
+        __syncwarp();
         if (ok && (ok = wait(keys, 0) && wait(m_written, 0) && wait(t_free, heads - 1))) {
             tc::fence_after();
             constexpr uint32_t id_c = tc::idesc(64, false, true), id_b = tc::idesc(64, true, true);
+            const uint64_t md = tc::desc(sm, 16), mt = tc::desc(sm, kX), kd = tc::desc(sk, 16);
+            if (tc::elect()) {
 #pragma unroll
-            for (int ks = 0; ks < kChunk / 16; ++ks)
-                tc::mma(tmem + kT, tc::desc(sm + (ks / 4) * kX + (ks % 4) * 32, 16), tc::desc(sk + ks * 2048, 16), id_c, ks);
+                for (int ks = 0; ks < kChunk / 16; ++ks) tc::mma(tmem + kT, md + (((ks / 4) * kX + (ks % 4) * 32) >> 4), kd + ks * 128, id_c, ks);
 #pragma unroll
-            for (int ks = 0; ks < kChunk / 16; ++ks)
-                tc::mma(tmem + kT + 64, tc::desc(sm + ks * 2048, kX), tc::desc(sk + kX + ks * 2048, 16), id_b, ks);
-            tc::commit(f_done);
+                for (int ks = 0; ks < kChunk / 16; ++ks) tc::mma(tmem + kT + 64, mt + ks * 128, kd + ((kX + ks * 2048) >> 4), id_b, ks);
+                tc::commit(f_done);
+            }
+            __syncwarp();
         }
         if (!ok) {  // left early: no box may still be on its way when the block ends
-            atomicOr(p.flag, kFlagTimeout);
             for (int i = 0; i < kStages; ++i)
                 for (int k = 0; k < 2; ++k) mbar_wait(loaded + 8 * i, k, kDrainIters);
             mbar_wait(keys, 0, kDrainIters);

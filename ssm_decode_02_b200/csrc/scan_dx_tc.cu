@@ -511,63 +511,76 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                 p.part[static_cast<long long>(p.slots) * p.H + cells0 + h] = dd;
             }
         }
-    } else if (lane == 0) {
-        auto wait = [&](uint32_t b, int phase) { return mbar_wait(b, phase & 1, kWaitIters); };
+    } else {
+        auto wait = [&](uint32_t b, int phase) { return tc::wait_warp(b, phase, p.flag); };
         bool ok = wait(keys, 0);
+        const uint64_t bd = tc::desc(sb, 16), cd = tc::desc(sc, 16), stage0 = tc::desc(stages, 16), unit0 = tc::desc(units, 16);
         if (ok) {
             tc::fence_after();
             constexpr uint32_t id = tc::idesc(kChunk, false, false);
+            if (tc::elect()) {
 #pragma unroll
-            for (int ks = 0; ks < N / 16; ++ks) {
-                const uint32_t o = (ks / 4) * kChunk * 128 + (ks % 4) * 32;
-                tc::mma(tmem + kG, tc::desc(sb + o, 16), tc::desc(sc + o, 16), id, ks);
+                for (int ks = 0; ks < N / 16; ++ks) {
+                    const uint32_t o = ((ks / 4) * kChunk * 128 + (ks % 4) * 32) >> 4;
+                    tc::mma(tmem + kG, bd + o, cd + o, id, ks);
+                }
+                tc::commit(g_done);
             }
-            tc::commit(g_done);
+            __syncwarp();
         }
         constexpr uint32_t id_w = tc::idesc(kChunk, false, false), id = tc::idesc(kTile, false, true);
-        int unit = 0;
+        int unit = 0, head = 0, tile = 0;
         for (int it = 0; it < items && ok; ++it) {
-            const int head = it / p.tiles, tile = it - head * p.tiles;
             if (tile == 0) {
                 if (head && !(ok = wait(w_free, head - 1))) break;
                 for (int t = 0; t < p.tiles && ok; ++t) {
                     if (!(ok = wait(loaded + 8 * ((it + t) & 1), (it + t) / 2))) break;
                     tc::fence_after();
-                    const uint32_t sx = stages + ((it + t) & 1) * 2 * Sh::kX;
+                    const uint64_t xd = stage0 + ((it + t) & 1) * (2 * Sh::kX >> 4), yd = xd + (Sh::kX >> 4);
+                    if (tc::elect()) {
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) tc::mma(tmem + kW, tc::desc(sx + ks * 32, 16), tc::desc(sx + Sh::kX + ks * 32, 16), id_w, t || ks);
+                        for (int ks = 0; ks < 4; ++ks) tc::mma(tmem + kW, xd + ks * 2, yd + ks * 2, id_w, t || ks);
+                        if (t == p.tiles - 1) tc::commit(w_done);
+                    }
+                    __syncwarp();
                 }
                 if (!ok) break;
-                tc::commit(w_done);
             }
             if (it && !(ok = wait(cd_free, it - 1) && wait(e_free, it - 1))) break;
             for (int part = 0; part < N / 64 && ok; ++part)
                 for (int which = 0; which < 2 && ok; ++which, ++unit) {
                     if (!(ok = wait(unit_written + 8 * (unit % kUnits), unit / kUnits))) break;
                     tc::fence_after();
-                    const uint32_t a = (which ? sc : sb) + part * kChunk * 128, b = units + (unit % kUnits) * kUnit;
+                    const uint64_t a = (which ? cd : bd) + part * (kChunk * 128 >> 4), b = unit0 + (unit % kUnits) * (kUnit >> 4);
                     const uint32_t d = tmem + (which ? kE : kDd);
-                    const uint64_t da = tc::desc(a, 16), db = tc::desc(b, 16);
-#pragma unroll 1
-                    for (int m = 2; m >= 0; --m)
+                    if (tc::elect()) {
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            tc::mma(d, da + ks * 2, db + ((m * kPlane + ks * 2048) >> 4), id, part || m != 2 || ks);
-                    tc::commit(unit_free + 8 * (unit % kUnits));
+                        for (int m = 2; m >= 0; --m)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                tc::mma(d, a + ks * 2, b + ((m * kPlane + ks * 2048) >> 4), id, m != 2 || ks || part);
+                        tc::commit(unit_free + 8 * (unit % kUnits));
+                    }
+                    __syncwarp();
                 }
             if (!ok) break;
-            tc::commit(e_done);
+            if (tc::elect()) tc::commit(e_done);
+            __syncwarp();
             if (tile == 0 && !(ok = wait(pt_written, head))) break;
             tc::fence_after();
-            const uint32_t sy = stages + (it & 1) * 2 * Sh::kX + Sh::kX;
-            const uint64_t dy = tc::desc(sy, 16);
-#pragma unroll 2
-            for (int ks = 0; ks < kChunk / 16; ++ks) tc::mma_ta(tmem + kC, tmem + kPt + ks * 8, dy + ks * 128, id, ks);
-            tc::commit(cd_done);
-            if (tile == p.tiles - 1) tc::commit(pt_free);
+            const uint64_t yd = stage0 + (((it & 1) * 2 + 1) * Sh::kX >> 4);
+            const bool last = tile == p.tiles - 1;
+            if (tc::elect()) {
+#pragma unroll
+                for (int ks = 0; ks < kChunk / 16; ++ks) tc::mma_ta(tmem + kC, tmem + kPt + ks * 8, yd + ks * 128, id, ks);
+                tc::commit(cd_done);
+                if (last) tc::commit(pt_free);
+            }
+            __syncwarp();
+            tile = last ? 0 : tile + 1;
+            head += last;
         }
         if (!ok) {  // left early: no box may still be on its way when the block ends
-            atomicOr(p.flag, kFlagTimeout);
             for (int i = 0; i < 2; ++i)
                 for (int k = 0; k < 2; ++k) mbar_wait(loaded + 8 * i, k, kDrainIters);
             mbar_wait(keys, 0, kDrainIters);

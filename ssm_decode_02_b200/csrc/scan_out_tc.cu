@@ -286,38 +286,53 @@ __global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant
                 announce(b);
             }
         }
-    } else if (lane == 0) {
-        bool ok = mbar_wait(keys, 0, kWaitIters);
+    } else {
+        bool ok = tc::wait_warp(keys, 0, p.flag);
+        const uint64_t cd = tc::desc(sc, 16), bd = tc::desc(sb, 16), stage0 = tc::desc(stages, 16);
         if (ok) {
+            tc::fence_after();
             constexpr uint32_t id = tc::idesc(kChunk, false, false);
+            if (tc::elect()) {
 #pragma unroll
-            for (int ks = 0; ks < N / 16; ++ks) {
-                const uint32_t o = (ks / 4) * kChunk * 128 + (ks % 4) * 32;
-                tc::mma(tmem, tc::desc(sc + o, 16), tc::desc(sb + o, 16), id, ks);
+                for (int ks = 0; ks < N / 16; ++ks) {
+                    const uint32_t o = ((ks / 4) * kChunk * 128 + (ks % 4) * 32) >> 4;
+                    tc::mma(tmem, cd + o, bd + o, id, ks);
+                }
+                tc::commit(scores);
             }
-            tc::commit(scores);
+            __syncwarp();
         }
         constexpr uint32_t id = tc::idesc(kTile, false, true);
+        int head = 0, tile = 0;
         for (int it = 0; it < items && ok; ++it) {
-            const int head = it / p.tiles, tile = it % p.tiles, buf = head & 1;
-            const uint32_t st = stages + (it % kStages) * Sh::kStage, d = tmem + kD + (it & 1) * 128;
-            if (!(ok = mbar_wait(loaded + 8 * (it % kStages), (it / kStages) & 1, kWaitIters))) break;
-            if (it >= 2 && !(ok = mbar_wait(tile_free + 8 * (it & 1), (it / 2 - 1) & 1, kWaitIters))) break;
+            const int buf = head & 1;
+            const uint64_t sd = stage0 + (it % kStages) * (Sh::kStage >> 4);
+            const uint32_t d = tmem + kD + (it & 1) * 128;
+            if (!(ok = tc::wait_warp(loaded + 8 * (it % kStages), it / kStages, p.flag))) break;
+            if (it >= 2 && !(ok = tc::wait_warp(tile_free + 8 * (it & 1), it / 2 - 1, p.flag))) break;
             tc::fence_after();
+            if (tc::elect()) {
 #pragma unroll
-            for (int ks = 0; ks < N / 16; ++ks)
-                tc::mma(d, tc::desc(sc + (ks / 4) * kChunk * 128 + (ks % 4) * 32, 16), tc::desc(st + Sh::kX + ks * 2048, 16), id, ks);
+                for (int ks = 0; ks < N / 16; ++ks)
+                    tc::mma(d, cd + (((ks / 4) * kChunk * 128 + (ks % 4) * 32) >> 4), sd + ((Sh::kX + ks * 2048) >> 4), id, ks);
+            }
+            __syncwarp();
             if (tile == 0) {
-                if (!(ok = mbar_wait(left + 8 * buf, (head / 2) & 1, kWaitIters))) break;
+                if (!(ok = tc::wait_warp(left + 8 * buf, head / 2, p.flag))) break;
                 tc::fence_after();
             }
+            const bool last = tile == p.tiles - 1;
+            if (tc::elect()) {
 #pragma unroll
-            for (int ks = 0; ks < kChunk / 16; ++ks) tc::mma_ta(d + 64, tmem + kLeft + buf * 64 + ks * 8, tc::desc(st + ks * 2048, 16), id, ks);
-            tc::commit(tile_done + 8 * (it & 1));
-            if (tile == p.tiles - 1) tc::commit(left_free + 8 * buf);
+                for (int ks = 0; ks < kChunk / 16; ++ks) tc::mma_ta(d + 64, tmem + kLeft + buf * 64 + ks * 8, sd + ks * 128, id, ks);
+                tc::commit(tile_done + 8 * (it & 1));
+                if (last) tc::commit(left_free + 8 * buf);
+            }
+            __syncwarp();
+            tile = last ? 0 : tile + 1;
+            head += last;
         }
         if (!ok) {  // left early: no box may still be on its way when the block ends
-            atomicOr(p.flag, kFlagTimeout);
             for (int i = 0; i < kStages; ++i)
                 for (int k = 0; k < 2; ++k) mbar_wait(loaded + 8 * i, k, kDrainIters);
             mbar_wait(keys, 0, kDrainIters);

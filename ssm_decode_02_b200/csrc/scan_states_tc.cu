@@ -242,26 +242,30 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < R; ++i) end[(ps.local ? seg_at : at0) + static_cast<long long>(i) * p.P] = S[i];
         }
-    } else if (lane == 0) {
+    } else {
         constexpr uint32_t id = tc::idesc(N, true, true);
+        const uint64_t keys0 = tc::desc(base, 8192), terms0 = tc::desc(terms, 8192);
         for (int s = 0; s < steps; ++s) {
-            bool ok = mbar_wait(written + 8 * (s & 1), (s / 2) & 1, kWaitIters);
-            if (ok && !(s & 1) && s >= 4) ok = mbar_wait(taken + 8 * ((s / 2) & 1), (s / 4 - 1) & 1, kWaitIters);
-            if (!ok) {
-                atomicOr(p.flag, kFlagTimeout);
-                break;
-            }
+            if (!tc::wait_warp(written + 8 * (s & 1), s / 2, p.flag)) break;
+            if (!(s & 1) && s >= 4 && !tc::wait_warp(taken + 8 * ((s / 2) & 1), s / 4 - 1, p.flag)) break;
             tc::fence_after();
-            const uint32_t st = base + (s % kStages) * Sh::kStage, tb = terms + (s & 1) * Sh::kTerms;
+            const uint64_t kd = keys0 + (s % kStages) * (Sh::kStage >> 4), td = terms0 + (s & 1) * (Sh::kTerms >> 4);
             const uint32_t d = tmem + ((s / 2) & 1) * N;
+            if (tc::elect()) {
 #pragma unroll
-            for (int ks = 0; ks < kHalf / 16; ++ks)
+                for (int ks = 0; ks < kHalf / 16; ++ks)
 #pragma unroll
-                for (int k = 2; k >= 0; --k)
-                    tc::mma(d, tc::desc(tb + k * Sh::kValues + ks * 2048, 8192), tc::desc(st + ks * 2048, 8192), id,
-                            (s & 1) || ks || k != 2);
-            tc::commit(done + 8 * (s & 1));
-            if (s & 1) tc::commit(full + 8 * ((s / 2) & 1));
+                    for (int k = 2; k >= 0; --k) {
+                        const uint64_t ad = td + ((k * Sh::kValues + ks * 2048) >> 4), bd = kd + ks * 128;
+                        if (ks == 0 && k == 2)
+                            tc::mma(d, ad, bd, id, s & 1);
+                        else
+                            tc::mma(d, ad, bd, id, true);
+                    }
+                tc::commit(done + 8 * (s & 1));
+                if (s & 1) tc::commit(full + 8 * ((s / 2) & 1));
+            }
+            __syncwarp();
         }
     }
     tc::fence_before();

@@ -91,6 +91,14 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool a_mn, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
            (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
+// One lane of a converged warp.  The issuing warps stay together and enter only the
+// products this way: descriptors are then computed once for the warp (uniform
+// registers); one lane on its own took about 100 cycles per product to issue them.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
 // D[128 x n] (+)= A B, one thread.
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool add) {
     asm volatile(
