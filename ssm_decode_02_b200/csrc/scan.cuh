@@ -28,6 +28,7 @@ using bf16 = __nv_bfloat16;
 constexpr int kChunk = 128;   // tokens of a chunk
 constexpr int kTile = 64;     // state columns of a block's tile
 constexpr int kThreads = 256;
+constexpr int kSms = 148;     // of a B200
 // log2 of a decay of zero: far below any exponent, so that its power is 0, and
 // small enough that sums of 128 keep every other term in twice binary32
 constexpr double kLogZero = -1e5;

@@ -10,7 +10,6 @@ namespace rsq {
 namespace scan {
 namespace {
 
-constexpr int kSms = 148;
 constexpr int64_t kMaxTokens = (1LL << 31) - (1LL << 17);
 // Longest sequences (equal lengths) that the token-by-token kernel takes.
 constexpr int kStepTokens = 4;
@@ -57,13 +56,16 @@ size_t layout(const rsq_scan_config& c, bool backward, Params* p, uint8_t* base)
         return c.ragged ? p->tokens / unit + p->n : p->n * ((p->len + unit - 1) / unit);
     };
     p->slots = slots_of(kChunk);
-    // Segments where the sequences alone leave SMs idle: twice the work on the
-    // states for as many more blocks.
-    const long long blocks = static_cast<long long>(p->n) * p->H * p->tiles * (backward ? 2 : 1);
-    const int chunks = p->slots / p->n;
+    // Segments where the sequences alone leave half of the SMs idle: twice the work on
+    // the states, spread over as many blocks as run at once (a few more would take as
+    // long as twice as many).
+    const bool tc = states_tc_ok(*p);
+    const long long blocks = static_cast<long long>(p->n) * (backward ? 2 : 1) *
+                             (tc ? p->H * p->P / 128 * std::max(1, p->N / 128) : p->H * p->tiles);
+    const int chunks = p->slots / p->n, fit = (tc ? 1 : 2) * kSms;
     p->seg_chunks = 0;
-    if (blocks * 4 <= 2 * kSms && chunks >= 16) {
-        const int want = static_cast<int>((2 * kSms + blocks - 1) / blocks);
+    if (blocks * 4 <= fit && chunks >= 16) {
+        const int want = static_cast<int>(fit / blocks);
         p->seg_chunks = std::max(4, (chunks + want - 1) / want);
         if (p->seg_chunks * 2 > chunks) p->seg_chunks = 0;
     }
@@ -137,16 +139,17 @@ rsq_status check_workspace(const char* who, size_t need, const void* ws, size_t 
     return RSQ_OK;
 }
 
-// Heads of a block of the chunk kernels, one block per SM at a time: the split with
-// the fewest rounds times their length, where a block begins with work that is worth
-// about two more heads (keys, scores).
-int head_set(const Params& p) {
+// Heads of a unit of the chunk kernels, of which an SM works on one at a time: the
+// split with the fewest rounds times their length.  `start`: what the beginning of a
+// unit (keys, scores) is worth in quarters of a head's tile -- two tiles where a block
+// has one unit, little where the next one's beginning is hidden behind the last heads.
+int head_set(const Params& p, int start) {
     const long long chunks = std::max(1, p.tokens / kChunk);
     int best = p.per;
     long long least = -1;
     for (int set = p.per; set >= 1; --set) {
         const long long blocks = chunks * p.G * ((p.per + set - 1) / set);
-        const long long cost = (blocks + kSms - 1) / kSms * (set * p.tiles + 2);
+        const long long cost = (blocks + kSms - 1) / kSms * (4 * set * p.tiles + start);
         if (least < 0 || cost < least) {
             least = cost;
             best = set;
@@ -238,7 +241,7 @@ rsq_status rsq_scan(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs, c
     int err = maps_for(p, false, &m);
     if (!err && p.slots) err = launch_gates(p, s);
     if (!err) err = launch_states(p, m, false, s);
-    if (!err && p.slots) err = launch_out(p, m, head_set(p), s);
+    if (!err && p.slots) err = launch_out(p, m, head_set(p, out_tc_ok(p) ? 1 : 8), s);
     return done("scan", err);
 }
 
@@ -277,7 +280,7 @@ rsq_status rsq_scan_backward(const rsq_scan_config* cfg, const rsq_scan_inputs* 
     int err = maps_for(p, true, &m);
     if (!err && p.slots) err = launch_gates(p, s);
     if (!err) err = launch_states(p, m, true, s);
-    if (!err) err = launch_backward(p, m, head_set(p), s);
+    if (!err) err = launch_backward(p, m, head_set(p, 8), s);
     return done("scan_backward", err);
 }
 

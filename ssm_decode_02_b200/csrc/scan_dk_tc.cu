@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
                 const float2 bm = make_float2(__shfl_sync(0xffffffffu, bc[k].x, meet), __shfl_sync(0xffffffffu, bc[k].y, meet));
                 const float last = __shfl_sync(0xffffffffu, bc[k].x, 31);
                 const float r = ex2_diff(br, bm);
-                const bool direct = diagonal && !(bm.x - last < 60.f);
+                const bool direct = diagonal && !(bm.x - last < 100.f);
                 __syncwarp();
                 fac[k * 32 + lane] = dt[k] * ex2_diff(bm, bc[k]);
                 if (direct) pair[lane] = make_float4(bc[k].x, bc[k].y, dt[k], 0.f);

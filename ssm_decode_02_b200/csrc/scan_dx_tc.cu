@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                 const float2 bm = make_float2(__shfl_sync(0xffffffffu, bk.x, meet), __shfl_sync(0xffffffffu, bk.y, meet));
                 const float first = __shfl_sync(0xffffffffu, bk.x, 0);
                 const float r = ex2_diff(bm, br);
-                const bool direct = diagonal && !(first - bm.x < 60.f);
+                const bool direct = diagonal && !(first - bm.x < 100.f);
                 __syncwarp();
                 fac[lane] = ex2_diff(bk, bm);
                 if (direct) pair[lane] = bk;
