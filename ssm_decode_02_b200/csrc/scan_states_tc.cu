@@ -7,8 +7,10 @@
 // of the weighted values, 128 x tokens in three bf16 terms (split3), with the keys,
 // tokens x N, is a tcgen05 product into one of two tensor-memory tiles.  Three kinds
 // of warps, which meet at mbarriers only:
-//   8 converters  have keys and values of half a chunk copied ahead (four stages),
-//                 weight the values and write their terms (two buffers);
+//   2 x 4 converters  have keys and values of half a chunk copied ahead (two stages
+//                 each), weight the values and write their terms; the two groups take
+//                 turns, so that the waits of one (copies, products, gates: three
+//                 quarters of its time) pass while the other works;
 //   8 updaters    hold the state, a thread half a column of N binary32; they store it
 //                 as the state before the chunk and take in the chunk's tile while the
 //                 next chunk's products run into the other;
@@ -74,7 +76,7 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            mbar_init(written + 8 * i, kConverters);
+            mbar_init(written + 8 * i, kConverters / 2);
             mbar_init(done + 8 * i, 1);
             mbar_init(full + 8 * i, 1);
             mbar_init(taken + 8 * i, kUpdaters);
@@ -88,9 +90,10 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
     const uint32_t tmem = *tmem_slot;
     auto chunk_of = [&](int s) { return ps.rev ? chunks - 1 - s / 2 : s / 2; };
     if (threadIdx.x < kConverters) {
-        // this thread's chunks: rows t and t + 32, columns 8 c.. of every 64 x 64 tile
-        const int t = threadIdx.x >> 3, c = threadIdx.x & 7;
-        const uint32_t place = tile_at<128>(t, c);  // row t + 32: 4096 bytes on
+        // this group's steps are those of its parity; this thread's chunks: rows t + 16 j,
+        // columns 8 c.. of every 64 x 64 tile
+        const int mine = warp >> 2, i0 = threadIdx.x & 127, t = i0 >> 3, c = i0 & 7;
+        const uint32_t place = tile_at<128>(t, c);  // row t + 16 j: 2048 j bytes on
         const bf16* kp = ps.k + static_cast<long long>(group) * p.N + row0 + c * 8;
         const bf16* vp = ps.v + c0 + c * 8;
         const int h1 = heads - 1;                   // head of columns 64..127, from h0
@@ -99,11 +102,11 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
         const CUtensorMap *kmap = ps.rev ? &maps.Cm : &maps.Bm, *vmap = ps.rev ? &maps.dout : &maps.x;
         auto load = [&](int s) {
             if (s < steps) {
-                const int row = chunk_of(s) * kChunk + (s & 1) * kHalf + t;
-                const uint32_t st = base + (s % kStages) * Sh::kStage + place;
-                const bool whole = row - t + kHalf <= len;
-                if (threadIdx.x == 0) {
-                    const uint32_t b = arrived + 8 * (s % kStages), to = base + (s % kStages) * Sh::kStage;
+                const int row = chunk_of(s) * kChunk + (s & 1) * kHalf;
+                const uint32_t to = base + (s % kStages) * Sh::kStage;
+                const bool whole = row + kHalf <= len;
+                if (i0 == 0) {
+                    const uint32_t b = arrived + 8 * (s % kStages);
                     if (whole) {
                         mbar_arrive_expect_tx(b, Sh::kStage);
 #pragma unroll
@@ -114,22 +117,22 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
                         mbar_arrive(b);
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 2 && !whole; ++j) {
-                    const bool on = row + 32 * j < len;
-                    const long long at = lo + (on ? row + 32 * j : 0);
+#pragma unroll 1
+                for (int j = 0; j < 4 && !whole; ++j) {
+                    const bool on = row + t + 16 * j < len;
+                    const long long at = lo + (on ? row + t + 16 * j : 0);
                     const bf16 *ksrc = kp + at * ps.ks, *vsrc = vp + at * ps.vs;
 #pragma unroll
-                    for (int b = 0; b < N / 64; ++b) cp16(st + j * 4096 + b * 8192, ksrc + b * 64, on);
+                    for (int b = 0; b < N / 64; ++b) cp16(to + place + j * 2048 + b * 8192, ksrc + b * 64, on);
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) cp16(st + Sh::kKeys + j * 4096 + b * 8192, vsrc + b * 64, on);
+                    for (int b = 0; b < 2; ++b) cp16(to + place + Sh::kKeys + j * 2048 + b * 8192, vsrc + b * 64, on);
                 }
             }
             cp_commit();
         };
-        // gates of the two rows for the two column tiles, read a step ahead
-        float2 gb[2][2], ge[2];
-        float gd[2][2];
+        // gates of the four rows for the two column tiles, read a step ahead
+        float2 gb[2][4], ge[2];
+        float gd[2][4];
         auto read_gates = [&](int s) {
             if (s >= steps) return;
 #pragma unroll
@@ -137,33 +140,33 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
                 const long long at = (static_cast<long long>(slot0 + chunk_of(s)) * p.H + h0 + b * h1) * kChunk;
                 ge[b] = p.gb[at + kChunk - 1];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    gb[b][j] = p.gb[at + (s & 1) * kHalf + t + 32 * j];
-                    gd[b][j] = p.gdt[at + (s & 1) * kHalf + t + 32 * j];
+                for (int j = 0; j < 4; ++j) {
+                    gb[b][j] = p.gb[at + (s & 1) * kHalf + t + 16 * j];
+                    gd[b][j] = p.gdt[at + (s & 1) * kHalf + t + 16 * j];
                 }
             }
         };
-        load(0);
-        load(1);
-        read_gates(0);
-        int s = 0;
-        for (; s < steps; ++s) {
-            float w[2][2];
+        load(mine);
+        read_gates(mine);
+        int s = mine;
+        for (; s < steps; s += 2) {
+            float w[2][4];
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) w[b][j] = ps.rev ? ex2(gb[b][j].x + gb[b][j].y) : ex2_diff(ge[b], gb[b][j]) * gd[b][j];
-            read_gates(s + 1);
+                for (int j = 0; j < 4; ++j) w[b][j] = ps.rev ? ex2(gb[b][j].x + gb[b][j].y) : ex2_diff(ge[b], gb[b][j]) * gd[b][j];
+            read_gates(s + 2);
+            // the products of step s - 2 are done with the terms' buffer and with the stage loaded next
+            if (s >= 2 && !tc::wait_warp(done + 8 * mine, s / 2 - 1, p.flag)) break;
+            load(s + 2);
             cp_wait<1>();
             if (!tc::wait_warp(arrived + 8 * (s % kStages), s / kStages, p.flag)) break;
-            // the products of step s - 2 are done with the terms' buffer and with the stage loaded below
-            if (s >= 2 && !tc::wait_warp(done + 8 * (s & 1), s / 2 - 1, p.flag)) break;
-            const uint32_t st = base + (s % kStages) * Sh::kStage + Sh::kKeys + place, tb = terms + (s & 1) * Sh::kTerms + place;
+            const uint32_t st = base + (s % kStages) * Sh::kStage + Sh::kKeys + place, tb = terms + mine * Sh::kTerms + place;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t o = b * 8192 + j * 4096;
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t o = b * 8192 + j * 2048;
                     uint32_t x[4], r[3][4];
                     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(st + o));
 #pragma unroll
@@ -176,13 +179,12 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
                                      : "memory");
                 }
             tc::fence_smem();
-            mbar_arrive(written + 8 * (s & 1));
-            load(s + 2);
+            mbar_arrive(written + 8 * mine);
         }
         cp_wait<0>();
         // left early: no box may still be on its way when the block ends
-        if (threadIdx.x == 0)
-            for (int k = s; k < min(s + 2, steps); ++k) mbar_wait(arrived + 8 * (k % kStages), (k / kStages) & 1, kDrainIters);
+        if (i0 == 0)
+            for (int k = s; k < min(s + 4, steps); k += 2) mbar_wait(arrived + 8 * (k % kStages), (k / kStages) & 1, kDrainIters);
     } else if (threadIdx.x < kConverters + kUpdaters) {
         // value column m (the tensor-memory lane), state rows n0 .. n0 + R - 1 of the block's
         constexpr int R = N / 2;
