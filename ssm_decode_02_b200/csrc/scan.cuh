@@ -261,6 +261,101 @@ __device__ __forceinline__ void store_rows(bf16* dst, long long stride, int row0
     }
 }
 
+// ---------------------------------------------------------------------------
+// The gradients of a head's gates over one chunk, by one warp: lane l has tokens 4 l
+// .. 4 l + 3.  With the tokens in NB blocks,
+//   col[b][t] = sum over j < t of block b of Z_tj,   row[a][t] = sum over i > t of block a of Z_it / dt_t
+// (Z and the other sums: scan_backward.cu).  The pairs (i, j) around a token t of
+// block c, i >= t > j, are those of whole blocks around c, of later blocks with the
+// tokens of c before t, of the tokens of c from t on with earlier blocks, and pairs
+// within c.  Only the last are had as a difference (every pair of c from t on, less
+// the pairs on t's one side): over a whole chunk the difference of two such sums
+// left ten times the rounding error in dA, a sum over the tokens.
+// ---------------------------------------------------------------------------
+struct HeadSums {
+    const float* col;
+    const float* row;
+    const float* own;   // Z_tt / dt_t
+    const float* in;
+    const float* fin;
+    const float* dot;   // x_t.dout_t
+    float through;      // 2^b_end <S_0, dS>
+};
+
+template <int NB>
+__device__ __forceinline__ void head_gates(const HeadSums& s, const float (&dt)[4], int valid, int lane, float (&dlog)[4],
+                                           float (&dir)[4], float& dot) {
+    constexpr int BS = kChunk / NB, LB = 32 / NB;   // tokens and lanes of a block
+    const int c = lane / LB;
+    float suf[4], pre[4], ins[4], fi[4];
+    dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int t = lane * 4 + k;
+        suf[k] = pre[k] = ins[k] = fi[k] = dir[k] = 0.f;
+        if (t >= valid) continue;
+        float before = 0.f, after = 0.f;
+        for (int b = 0; b < c; ++b) before += s.col[b * kChunk + t];
+        for (int a = c + 1; a < NB; ++a) after += s.row[a * kChunk + t];
+        const float within = s.row[c * kChunk + t];
+        suf[k] = before + (s.col[c * kChunk + t] - dt[k] * within);
+        pre[k] = dt[k] * after;
+        ins[k] = s.in[t];
+        fi[k] = dt[k] * s.fin[t];
+        dir[k] = ((after + within) + s.own[t]) + s.fin[t];
+        dot += s.dot[t];
+    }
+    // whole blocks around block c
+    float around = 0.f;
+#pragma unroll 1
+    for (int m = 1; m < NB - 1; ++m) {
+        float v = 0.f;
+        for (int i = (m + 1) * BS + lane; i < valid; i += 32)
+            for (int b = 0; b < m; ++b) v += s.col[b * kChunk + i];
+#pragma unroll
+        for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+        if (m == c) around = v;
+    }
+    // sums of the lanes behind (suf, ins) and before (pre, fi), within the block and over all
+    const float s0 = (suf[0] + suf[1]) + (suf[2] + suf[3]), p0 = (pre[0] + pre[1]) + (pre[2] + pre[3]);
+    const float i0 = (ins[0] + ins[1]) + (ins[2] + ins[3]), f0 = (fi[0] + fi[1]) + (fi[2] + fi[3]);
+    float sb = __shfl_down_sync(0xffffffffu, s0, 1, LB), pb = __shfl_up_sync(0xffffffffu, p0, 1, LB);
+    float ib = __shfl_down_sync(0xffffffffu, i0, 1), fb = __shfl_up_sync(0xffffffffu, f0, 1);
+    if (lane % LB == LB - 1) sb = 0.f;
+    if (lane % LB == 0) pb = 0.f;
+    if (lane == 31) ib = 0.f;
+    if (lane == 0) fb = 0.f;
+#pragma unroll
+    for (int d = 1; d < LB; d <<= 1) {
+        const float a = __shfl_down_sync(0xffffffffu, sb, d, LB), b = __shfl_up_sync(0xffffffffu, pb, d, LB);
+        if (lane % LB + d < LB) sb += a;
+        if (lane % LB >= d) pb += b;
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const float a = __shfl_down_sync(0xffffffffu, ib, d), b = __shfl_up_sync(0xffffffffu, fb, d);
+        if (lane + d < 32) ib += a;
+        if (lane >= d) fb += b;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    float up_p = pb, up_f = fb;
+    float down_s[4], down_i[4];
+#pragma unroll
+    for (int k = 3; k >= 0; --k) {
+        sb += suf[k];
+        ib += ins[k];
+        down_s[k] = sb;
+        down_i[k] = ib;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        dlog[k] = ((down_s[k] + up_p) + around) + ((down_i[k] + up_f) + s.through);
+        up_p += pre[k];
+        up_f += fi[k];
+    }
+}
+
 // One direction of the state recurrence.
 struct Pass {
     const bf16* k;          // key rows: Bm | Cm

@@ -9,8 +9,8 @@
 // the gradients of the gates are
 //     dlog a_t = sum_{t'>=t} m_t' + sum_{j<t} dt_j fin_j + 2^b_end <S_0, dS>
 //     ddt_t    = sum_{i>=t} L_it (C_i.B_t)(dout_i.x_t) + fin_t + A dlog a_t
-// (pairs on one side of t cancel in the first sum; the diagonal, which is on no
-// side, is left out of it).  They are binary32 outputs: Z comes from products of the inputs alone, and the
+// (pairs on one side of t cancel in the first sum, which is therefore made from sums
+// by blocks, head_gates in scan.cuh).  They are binary32 outputs: Z comes from products of the inputs alone, and the
 // two state terms from states in three bf16 terms (split3).
 #include "tc.cuh"
 
@@ -67,7 +67,7 @@ struct DxShape {
     static constexpr int kX = kChunk * kTile * 2;
     static constexpr int kRows = N < 128 ? N : 128;             // state rows staged at a time
     static constexpr int kPlanes = 3 * kRows * kTile * 2;
-    static constexpr int kSmall = kChunk * (8 + 4) + 8 * kChunk * 4 + 5 * kChunk * 4 + 64;
+    static constexpr int kSmall = kChunk * (8 + 4) + 16 * kChunk * 4 + 4 * kChunk * 4 + 64;
     static constexpr int kSmem = 2 * kK + 2 * kX + kPlanes + kSmall;
 };
 
@@ -94,12 +94,12 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
     float2* b = reinterpret_cast<float2*>(smem + 2 * Sh::kK + 2 * Sh::kX + Sh::kPlanes);
     float* dt = reinterpret_cast<float*>(b + kChunk);
     float* zrow = dt + kChunk;           // [8][kChunk] sum_{j<i} Z_ij by the warps of j
-    float* in_i = zrow + 8 * kChunk;     // 2^b_i C_i.(S_0 dout_i)
-    float* dir = in_i + kChunk;          // ddt without the decay's part
-    float* fin = dir + kChunk;           // 2^(b_end-b_j) B_j.(dS x_j)
+    float* zcol = zrow + 8 * kChunk;     // [8][kChunk] sum_{i>j} Z_ij / dt_j by the blocks of 16 i
+    float* in_i = zcol + 8 * kChunk;     // 2^b_i C_i.(S_0 dout_i)
+    float* own = in_i + kChunk;          // Z_jj / dt_j
+    float* fin = own + kChunk;           // 2^(b_end-b_j) B_j.(dS x_j)
     float* row_d = fin + kChunk;         // x_i.dout_i
-    float* off = row_d + kChunk;         // dir without the state's part and the diagonal
-    float* ends = off + kChunk;          // [8] <S_0, dS> by warp
+    float* ends = row_d + kChunk;          // [8] <S_0, dS> by warp
     const int valid = rg.valid;
     const int row0 = warp * 16;
     const bool live = row0 < valid;
@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
             b[threadIdx.x] = p.gb[gate_at + threadIdx.x];
             dt[threadIdx.x] = p.gdt[gate_at + threadIdx.x];
         }
-        for (int i = threadIdx.x; i < 8 * kChunk; i += kThreads) zrow[i] = 0.f;
-        float in0 = 0.f, in8 = 0.f, dir0 = 0.f, dir8 = 0.f, own0 = 0.f, own8 = 0.f, fin0 = 0.f, fin8 = 0.f, d0 = 0.f, d8 = 0.f, through = 0.f;
+        for (int i = threadIdx.x; i < 16 * kChunk; i += kThreads) zrow[i] = 0.f;  // and zcol
+        float in0 = 0.f, in8 = 0.f, own0 = 0.f, own8 = 0.f, fin0 = 0.f, fin8 = 0.f, d0 = 0.f, d8 = 0.f, through = 0.f;
         const float dh = p.D ? __ldg(p.D + h) : 0.f;
 
         for (int tile = 0; tile < p.tiles; ++tile) {
@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
                         mma(zz[1], xa[ks], v[2], v[3]);
                     }
                     uint32_t a[4];
+                    float dir0 = 0.f, dir8 = 0.f;
                     const float dt0 = dt[row0 + g], dt8 = dt[row0 + g + 8];
 #pragma unroll
                     for (int nb = 0; nb < 2; ++nb) {
@@ -245,6 +246,12 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
                         }
                         a[2 * nb] = pack(pr[0], pr[1]);
                         a[2 * nb + 1] = pack(pr[2], pr[3]);
+                    }
+                    dir0 = quad_sum(dir0);
+                    dir8 = quad_sum(dir8);
+                    if (q == 0) {
+                        zcol[ib * kChunk + row0 + g] += dir0;
+                        zcol[ib * kChunk + row0 + g + 8] += dir8;
                     }
 #pragma unroll
                     for (int c2 = 0; c2 < 4; ++c2) {
@@ -310,8 +317,6 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
         // row sums to shared memory, then the gates by the first warp
         in0 = quad_sum(in0);
         in8 = quad_sum(in8);
-        dir0 = quad_sum(dir0);
-        dir8 = quad_sum(dir8);
         own0 = quad_sum(own0);
         own8 = quad_sum(own8);
         fin0 = quad_sum(fin0);
@@ -324,10 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
             const float2 b0 = b[row0 + g], b8 = b[row0 + g + 8];
             in_i[row0 + g] = in0 * ex2(b0.x + b0.y);
             in_i[row0 + g + 8] = in8 * ex2(b8.x + b8.y);
-            dir[row0 + g] = (dir0 + own0) + fin0;
-            dir[row0 + g + 8] = (dir8 + own8) + fin8;
-            off[row0 + g] = dir0;
-            off[row0 + g + 8] = dir8;
+            own[row0 + g] = own0;
+            own[row0 + g + 8] = own8;
             fin[row0 + g] = fin0;
             fin[row0 + g + 8] = fin8;
             row_d[row0 + g] = d0;
@@ -336,54 +339,24 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
         if (lane == 0) ends[warp] = through;
         __syncthreads();
         if (warp == 0) {
-            float m[4], f[4], dd = 0.f;
+            HeadSums hs{zrow, zcol, own, in_i, fin, row_d, 0.f};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = lane * 4 + i;
-                float z = 0.f;
-                m[i] = f[i] = 0.f;
-                if (t >= valid) continue;
-#pragma unroll
-                for (int w = 0; w < 8; ++w) z += zrow[w * kChunk + t];
-                m[i] = (z + in_i[t]) - dt[t] * off[t];
-                f[i] = dt[t] * fin[t];
-                dd += row_d[t];
-            }
-            // m over the lanes behind this one, dt fin over the lanes before it
-            float after = __shfl_down_sync(0xffffffffu, m[0] + m[1] + m[2] + m[3], 1);
-            float before = __shfl_up_sync(0xffffffffu, f[0] + f[1] + f[2] + f[3], 1);
-            if (lane == 31) after = 0.f;
-            if (lane == 0) before = 0.f;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const float o = __shfl_down_sync(0xffffffffu, after, d), u = __shfl_up_sync(0xffffffffu, before, d);
-                if (lane + d < 32) after += o;
-                if (lane >= d) before += u;
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, d);
-            float thr = 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) thr += ends[w];
+            for (int w = 0; w < 8; ++w) hs.through += ends[w];
             const float2 be = b[kChunk - 1];
-            thr *= ex2(be.x + be.y);
-            f[3] = before + f[0] + f[1] + f[2];   // now sums over the tokens before
-            f[2] = before + f[0] + f[1];
-            f[1] = before + f[0];
-            f[0] = before;
+            hs.through *= ex2(be.x + be.y);
             const float ah = p.decay ? 0.f : __ldg(p.A + h);
-            float da = 0.f, run = after;
+            const float dt4[4] = {dt[lane * 4], dt[lane * 4 + 1], dt[lane * 4 + 2], dt[lane * 4 + 3]};
+            float dl[4], dir[4], dd, da = 0.f;
+            head_gates<8>(hs, dt4, valid, lane, dl, dir, dd);
 #pragma unroll
-            for (int i = 3; i >= 0; --i) {
-                const int t = lane * 4 + i;
-                run += m[i];
+            for (int k = 0; k < 4; ++k) {
+                const int t = lane * 4 + k;
                 if (t >= valid) continue;
-                float dl = (run + f[i]) + thr;
                 const long long at = static_cast<long long>(rg.first + t) * p.H + h;
-                if (p.decay && __ldg(p.decay + at) == 0.f) dl = 0.f;  // nothing passes: the sums only cancel to rounding
-                if (p.dlog) p.dlog[at] = dl;
-                if (p.ddt) p.ddt[at] = p.decay ? dir[t] : fmaf(ah, dl, dir[t]);
-                da = fmaf(dt[t], dl, da);
+                if (p.decay && __ldg(p.decay + at) == 0.f) dl[k] = 0.f;  // nothing passes: the sums only cancel to rounding
+                if (p.dlog) p.dlog[at] = dl[k];
+                if (p.ddt) p.ddt[at] = p.decay ? dir[k] : fmaf(ah, dl[k], dir[k]);
+                da = fmaf(dt4[k], dl[k], da);
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) da += __shfl_xor_sync(0xffffffffu, da, d);

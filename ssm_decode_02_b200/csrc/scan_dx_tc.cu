@@ -30,7 +30,7 @@ constexpr int kRaw = 64 * kTile * 4;            // the same rows in binary32, tw
 constexpr int kPlane = 64 * kTile * 2, kUnit = 3 * kPlane;
 constexpr int kG = 0, kW = 128, kC = 256, kDd = 320, kE = 384, kPt = 448;
 // sums of one head (floats)
-constexpr int kRow = 0, kOwn = 256, kCol = 384, kIn = 896, kFin = 1024, kDot = 1152, kThrough = 1280, kSums = 1288;
+constexpr int kRow = 0, kOwn = 512, kCol = 640, kIn = 1152, kFin = 1280, kDot = 1408, kThrough = 1536, kSums = 1544;
 
 template <int N>
 struct Shape {
@@ -143,7 +143,6 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
             if (i >= 2 && !(ok = tc::wait_warp(sums_free + 8 * (i & 1), i / 2 - 1, p.flag))) break;
             tc::fence_after();
             float* out = sums + (i & 1) * kSums;
-            float rows = 0.f;
 #pragma unroll 1   // the instruction cache holds the roles' loops only if they stay small
             for (int k = 0; k < 2; ++k) {
                 const int cols = half * 2 + k;                  // this block of 32 columns
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                 fac[lane] = ex2_diff(bk, bm);
                 if (direct) pair[lane] = bk;
                 __syncwarp();
-                float v[32], own = 0.f;
+                float v[32], own = 0.f, rows = 0.f;
                 uint32_t o[16];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
@@ -213,9 +212,9 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                 }
                 tc::tmem_st16(dst, o);
                 out[kCol + quarter * 128 + cols * 32 + lane] = transpose_sum(v, lane);
+                out[kRow + cols * 128 + row] = rows;
                 if (diagonal) out[kOwn + row] = own;
             }
-            out[kRow + half * 128 + row] = rows;
             tc::tmem_st_wait();
             tc::fence_before();
             mbar_arrive(w_free);
@@ -454,55 +453,23 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
             const float dt[4] = {dt4.x, dt4.y, dt4.z, dt4.w};
             if (!tc::wait_warp(sums_done + 8 * (i & 1), i / 2, p.flag)) break;
             const float* in = sums + (i & 1) * kSums;
-            float m[4], f[4], dir[4], dd = 0.f;
+            HeadSums hs{in + kCol, in + kRow, in + kOwn, in + kIn, in + kFin, in + kDot, 0.f};
+#pragma unroll
+            for (int w = 0; w < 8; ++w) hs.through += in[kThrough + w];
+            hs.through *= ex2(be.x + be.y);
+            float dl[4], dir[4], dd, da = 0.f;
+            head_gates<4>(hs, dt, valid, lane, dl, dir, dd);
+            __syncwarp();
+            mbar_arrive(sums_free + 8 * (i & 1));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int t = lane * 4 + k;
-                m[k] = f[k] = dir[k] = 0.f;
                 if (t >= valid) continue;
-                float z = 0.f;
-                for (int q = 0; q <= t / 32; ++q) z += in[kCol + q * 128 + t];
-                const float off = in[kRow + t] + in[kRow + 128 + t];
-                dir[k] = (off + in[kOwn + t]) + in[kFin + t];
-                m[k] = (z + in[kIn + t]) - dt[k] * off;
-                f[k] = dt[k] * in[kFin + t];
-                dd += in[kDot + t];
-            }
-            float thr = 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) thr += in[kThrough + w];
-            thr *= ex2(be.x + be.y);
-            __syncwarp();
-            mbar_arrive(sums_free + 8 * (i & 1));
-            // m over the lanes behind this one, dt fin over the lanes before it
-            float after = __shfl_down_sync(0xffffffffu, m[0] + m[1] + m[2] + m[3], 1);
-            float before = __shfl_up_sync(0xffffffffu, f[0] + f[1] + f[2] + f[3], 1);
-            if (lane == 31) after = 0.f;
-            if (lane == 0) before = 0.f;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const float o = __shfl_down_sync(0xffffffffu, after, d), u = __shfl_up_sync(0xffffffffu, before, d);
-                if (lane + d < 32) after += o;
-                if (lane >= d) before += u;
-            }
-#pragma unroll
-            for (int d = 16; d; d >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, d);
-            f[3] = before + f[0] + f[1] + f[2];   // now sums over the tokens before
-            f[2] = before + f[0] + f[1];
-            f[1] = before + f[0];
-            f[0] = before;
-            float da = 0.f, run = after;
-#pragma unroll
-            for (int k = 3; k >= 0; --k) {
-                const int t = lane * 4 + k;
-                run += m[k];
-                if (t >= valid) continue;
-                float dl = (run + f[k]) + thr;
                 const long long at = static_cast<long long>(rg.first + t) * p.H + h;
-                if (p.decay && __ldg(p.decay + at) == 0.f) dl = 0.f;  // nothing passes: the sums only cancel to rounding
-                if (p.dlog) p.dlog[at] = dl;
-                if (p.ddt) p.ddt[at] = p.decay ? dir[k] : fmaf(ah, dl, dir[k]);
-                da = fmaf(dt[k], dl, da);
+                if (p.decay && __ldg(p.decay + at) == 0.f) dl[k] = 0.f;  // nothing passes: the sums only cancel to rounding
+                if (p.dlog) p.dlog[at] = dl[k];
+                if (p.ddt) p.ddt[at] = p.decay ? dir[k] : fmaf(ah, dl[k], dir[k]);
+                da = fmaf(dt[k], dl[k], da);
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) da += __shfl_xor_sync(0xffffffffu, da, d);
