@@ -78,9 +78,13 @@ def step_bytes(w: W.Workload, head_bits, window: int = 0, key_axis: bool = False
 
 
 def source_hash() -> str:
+    """Of the sources that the decode kernels are built from (the scan's and the norms' are
+    not among them)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "ssm_decode_02_b200", "csrc")
     for f in sorted(os.listdir(csrc)):
+        if f.startswith(("scan", "norm", "tc.")):
+            continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
     return h.hexdigest()[:16]
@@ -737,6 +741,81 @@ def run_drift(args, w: W.Workload, pool) -> int:
     return 0
 
 
+def run_prompt(args, w: W.Workload) -> int:
+    """A Mamba-2 layer from prompt to decoding on one GPU, without its projections: residual
+    norm, scan over prompts of args.prompt tokens, gated norm, quantization of the states,
+    then decode steps with the gated norm on their output.  One JSON line."""
+    import torch
+    import ssm_decode_02_b200 as rsq
+
+    if w.family != "mamba2":
+        print("--prompt needs a Mamba-2 workload", file=sys.stderr)
+        return 2
+    dev = torch.device("cuda", 0)
+    B, H, N, P, G, T = w.B, w.H, w.dk, w.dv, w.ngroups, args.prompt
+    width, tokens = H * P, B * T
+    g = torch.Generator(device=dev)
+    g.manual_seed(w.input_seed)
+
+    def normal(*shape, dtype=torch.bfloat16, std=1.0, mean=0.0):
+        return (torch.randn(shape, generator=g, device=dev) * std + mean).to(dtype)
+
+    f32 = torch.float32
+    x, Bm, Cm = normal(tokens, H, P), normal(tokens, G, N), normal(tokens, G, N)
+    z, branch, residual = normal(tokens, width), normal(tokens, width // 2), normal(tokens, width // 2, dtype=f32)
+    dt = torch.nn.functional.softplus(normal(tokens, H, dtype=f32, mean=-2.0))
+    A, D = -torch.exp(2.8 * torch.rand(H, generator=g, device=dev)), normal(H, dtype=f32, std=0.1, mean=1.0)
+    w_in, w_out = torch.ones(width // 2, device=dev), torch.ones(width, device=dev)
+    scan = rsq.Scan(B, tokens, H, N, P, ngroups=G)
+    ws, out = scan.alloc_workspace(), torch.empty_like(x)
+    state = torch.empty((B, H, N, P), dtype=f32, device=dev)
+    y_in, y_out = torch.empty_like(branch), torch.empty_like(z)
+    ins = rsq.scan_inputs(x, Bm, Cm, dt, A, D)
+    pre = rsq.norm_config(branch, residual, torch.bfloat16)
+    post = rsq.norm_config(out.view(tokens, width), z, torch.bfloat16, order=rsq.RSQ_GATE_NORM)
+    bits = np.asarray(head_bits_of(w, rsq), np.int8)
+    ctx = rsq.Context(rsq.RSQ_MAMBA2, B, H, N, P, head_bits=bits, rounding=ROUNDING[w.rounding], seed=w.sr_seed, ngroups=G)
+    stored = ctx.alloc_state(dev)
+    step_ins = rsq.mamba2_inputs(x[:B].clone(), Bm[:B].clone(), Cm[:B].clone(), dt[:B].clone(), A, D)
+    step_out, step_z = torch.empty((B, H, P), dtype=f32, device=dev), z[:B].clone()
+    step_y = torch.empty_like(step_z)
+    step_norm = rsq.norm_config(step_out.view(B, width), step_z, torch.bfloat16, order=rsq.RSQ_GATE_NORM)
+
+    def prompt():
+        rsq.rsq_residual_norm(pre, branch, residual, None, w_in, residual, y_in)
+        scan.forward(ins, out, state_out=state, workspace=ws)
+        rsq.rsq_gated_norm(post, out.view(tokens, width), z, w_out, y_out)
+        ctx.quantize(state, stored)
+
+    def decode(t):
+        ctx.decode_step(stored, stored, step_ins, step_out, t)
+        rsq.rsq_gated_norm(step_norm, step_out.view(B, width), step_z, w_out, step_y)
+
+    def timed(f, n):
+        for t in range(max(3, min(args.warmup, 10))):
+            f(t)
+        ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        torch.cuda.synchronize()
+        ev[0].record()
+        for t in range(n):
+            f(t)
+        ev[1].record()
+        torch.cuda.synchronize()
+        return ev[0].elapsed_time(ev[1]) / n
+
+    steps = max(1, min(args.steps, 50))
+    prompt_ms = timed(lambda t: prompt(), steps)
+    rsq.rsq_scan_check(ws)
+    decode_ms = timed(decode, 4 * steps)
+    flags = ctx.check_flags()
+    emit({"metric": "prompt_tokens_per_s", "value": tokens / prompt_ms * 1e3, "unit": "tokens/s", "n_gpus": 1, "steps": steps,
+          "warmup": max(3, min(args.warmup, 10)), "ms_per_step": prompt_ms, "decode_ms_per_token": decode_ms, "flags": flags,
+          "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+          "config": {"model": "mamba2 layer without projections", "global_batch": B, "seq_len": T, "heads": H, "dk": N, "dv": P,
+                     "state": w.state, "l2": "inputs larger than L2", "parallelism": "dp1"}}, args)
+    return 0
+
+
 def step_input_bytes(w: W.Workload) -> int:
     esz = 2 if w.in_dtype == "bf16" else 4
     if w.family == "gdn":
@@ -797,6 +876,8 @@ def main():
     ap.add_argument("--seed", type=int, default=None, help="override the workload's stochastic-rounding seed")
     ap.add_argument("--chunk", type=int, default=0,
                     help="steps per captured CUDA graph (rounded to an even number of visits per layer)")
+    ap.add_argument("--prompt", type=int, default=0, metavar="TOKENS",
+                    help="a Mamba-2 workload's layer from prompts of so many tokens to decode steps instead of the bench")
     ap.add_argument("--sweep", action="store_true",
                     help="measure every row of the throughput table (one GPU), one line each")
     args = ap.parse_args()
@@ -812,6 +893,8 @@ def main():
         with mp.get_context("spawn").Pool(max(1, min(32, (os.cpu_count() or 2) - 1))) as pool:
             return run_drift(args, w, pool)
     w = W.BY_NAME[args.workload]
+    if args.prompt > 0:
+        return run_prompt(args, w)
     if args.rounding or args.seed is not None or args.state:
         import dataclasses
         if args.rounding:

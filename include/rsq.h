@@ -478,7 +478,7 @@ rsq_status rsq_pipe_streams(const rsq_pipe* pipe, void** copy_in, void** compute
  *   x   [tokens][heads][dv], Bm, Cm [tokens][ngroups][dk] in in_dtype; consecutive
  *       tokens lie x_stride, b_stride, c_stride elements apart (0: packed; else at
  *       least the row and a multiple of 8), so that they may be slices of one
- *       projection's output.
+ *       projection's output.  16-byte alignment, as the outputs and states.
  *   dt  float [tokens][heads] or NULL (1).  A, D  float [heads]; D NULL: 0.
  *   decay float [tokens][heads], values >= 0 (0 restarts the state), or NULL:
  *       exp(dt A), which needs dt and A.
@@ -508,8 +508,10 @@ rsq_status rsq_pipe_streams(const rsq_pipe* pipe, void** copy_in, void** compute
  *   of a_t; 0 where a_t is 0), dA (needs decay NULL), dD: float; dstate_in: float.
  *   dA and dD are sums over every sequence.  dstate_in may be dstate_out.
  * Both: asynchronous, capturable; errors RSQ_E_INVAL, RSQ_E_UNSUPPORTED, RSQ_E_CUDA.
- * Kernel attributes are set by the first call of a shape on a device: make it
- * before a stream capture begins. */
+ * rsq_scan_check: the scan's kernels wait for their own copies and products with a
+ *   limit; a kernel whose wait runs out marks the call's workspace and ends, its
+ *   outputs incomplete.  Synchronizes `stream` and returns RSQ_E_CUDA when the last
+ *   call with this workspace was so marked, else RSQ_OK.  Not capturable. */
 typedef struct {
     int family;
     int in_dtype;
@@ -554,6 +556,8 @@ rsq_status rsq_scan_backward(const rsq_scan_config* cfg, const rsq_scan_inputs* 
                              const int32_t* cu_seqlens, const float* state_in, const void* dout,
                              const float* dstate_out, const rsq_scan_grads* grads, void* workspace,
                              size_t workspace_bytes, void* stream);
+
+rsq_status rsq_scan_check(const void* workspace, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Norms around the mixer (no counterpart in the method's pages).

@@ -103,7 +103,7 @@ _EXPORTS = ["rsq_create", "rsq_destroy", "rsq_state_bytes", "rsq_head_offset", "
             "rsq_allocate_bits", "rsq_reduction_partials", "rsq_status_string", "rsq_last_error",
             "rsq_version", "rsq_decode_step_noalloc", "rsq_decode_step_copy_scale",
             "rsq_column_absmax", "rsq_window_bytes", "rsq_decode_step_window", "rsq_debug_waits",
-            "rsq_scan_workspace", "rsq_scan", "rsq_scan_backward", "rsq_norm_workspace",
+            "rsq_scan_workspace", "rsq_scan", "rsq_scan_backward", "rsq_scan_check", "rsq_norm_workspace",
             "rsq_gated_norm", "rsq_gated_norm_backward", "rsq_residual_norm",
             "rsq_residual_norm_backward"]
 
@@ -153,6 +153,7 @@ def _load():
                       ctypes.c_size_t, P], C),
         "rsq_scan_backward": ([ctypes.POINTER(rsq_scan_config), ctypes.POINTER(rsq_scan_inputs), P, P, P, P,
                                ctypes.POINTER(rsq_scan_grads), P, ctypes.c_size_t, P], C),
+        "rsq_scan_check": ([P, P], C),
         "rsq_norm_workspace": ([ctypes.POINTER(rsq_norm_config), ctypes.POINTER(ctypes.c_size_t)], C),
         "rsq_gated_norm": ([ctypes.POINTER(rsq_norm_config)] + [P] * 5, C),
         "rsq_gated_norm_backward": ([ctypes.POINTER(rsq_norm_config)] + [P] * 8 + [ctypes.c_size_t, P], C),
@@ -475,6 +476,11 @@ def rsq_scan_backward(cfg: rsq_scan_config, inputs: rsq_scan_inputs, dout, grads
     ws, n = _workspace(workspace)
     _check(lib.rsq_scan_backward(ctypes.byref(cfg), ctypes.byref(inputs), _dptr(cu_seqlens), _dptr(state_in),
                                  _dptr(dout), _dptr(dstate_out), ctypes.byref(grads), ws, n, _stream(stream)))
+
+
+def rsq_scan_check(workspace, stream=None) -> None:
+    """Raises when a kernel of the last call with this workspace gave up a wait."""
+    _check(lib.rsq_scan_check(_dptr(workspace), _stream(stream)))
 
 
 def rsq_norm_workspace(cfg: rsq_norm_config) -> int:

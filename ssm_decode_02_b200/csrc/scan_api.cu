@@ -245,6 +245,16 @@ rsq_status rsq_scan(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs, c
     return done("scan", err);
 }
 
+rsq_status rsq_scan_check(const void* workspace, void* stream) {
+    if (!workspace || misaligned(workspace)) return set_error(RSQ_E_INVAL, "scan_check: workspace null or not 16-byte aligned");
+    unsigned word = 0;   // the first of every layout
+    auto s = static_cast<cudaStream_t>(stream);
+    int err = cudaMemcpyAsync(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost, s);
+    if (!err) err = cudaStreamSynchronize(s);
+    if (err) return done("scan_check", err);
+    return word ? set_error(RSQ_E_CUDA, "scan_check: a bounded wait of the scan's kernels ran out") : RSQ_OK;
+}
+
 rsq_status rsq_scan_backward(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs, const int32_t* cu_seqlens,
                              const float* state_in, const void* dout, const float* dstate_out,
                              const rsq_scan_grads* grads, void* workspace, size_t workspace_bytes, void* stream) {

@@ -87,6 +87,7 @@ def test_scan_refuses_arguments():
     assert rsq.lib.rsq_scan_backward(ctypes.byref(s.cfg), ctypes.byref(_inputs()), None, None, P, None, None, P, back, None) == INVAL
     assert rsq.lib.rsq_scan_workspace(ctypes.byref(s.cfg), 2, ctypes.byref(ctypes.c_size_t())) == INVAL
     assert rsq.lib.rsq_scan_workspace(ctypes.byref(s.cfg), 0, None) == INVAL
+    assert rsq.lib.rsq_scan_check(None, None) == INVAL and rsq.lib.rsq_scan_check(P + 4, None) == INVAL
 
 
 def test_single_tokens_need_no_workspace():
