@@ -499,7 +499,7 @@ rsq_status rsq_pipe_streams(const rsq_pipe* pipe, void** copy_in, void** compute
  *   between calls; calls that may overlap need one each (captured graphs that
  *   run at the same time too).
  * rsq_scan: out [tokens][heads][dv]; state_in, state_out may be NULL, or the same
- *   buffer.
+ *   buffer.  No other output may overlap an input or another output.
  * rsq_scan_backward: given dout [tokens][heads][dv] (packed) and dstate_out (the
  *   gradient of state_out, NULL: 0), with the forward call's inputs and state_in.
  *   Writes what is not NULL of rsq_scan_grads: dx, dBm, dCm (packed, in_dtype; dBm

@@ -39,6 +39,7 @@ struct Params {
     int tiles;                    // column tiles of a head
     int ragged;
     int tokens, len;              // rows of the token arrays; length of a sequence (not ragged)
+    int steps;                    // ragged forward: sequences of so many tokens at most are step_kernel's
     const int32_t* cu;
     int slots;                    // chunk slots
     int seg_chunks, seg_slots;    // chunks of a segment (0: whole sequences), segment slots
@@ -55,6 +56,7 @@ struct Params {
     bf16* out;
     // workspace
     unsigned* flag;               // kFlagTimeout when a bounded wait ran out
+    int2* rows;                   // [slots] first row and number of rows, for all kernels after the gates'
     float2* gb;                   // [slots][H][kChunk] b_i in two floats
     float* gdt;                   // [slots][H][kChunk] dt
     bf16* sh;                     // forward: states before the chunks [slots][H][tiles][N][kTile]
@@ -120,9 +122,18 @@ __device__ __forceinline__ Range slot_range(const Params& p, int slot, int unit)
     r.seq = b;
     r.index = slot - first_slot(p, b, r.seq_first, unit);
     const long long at = static_cast<long long>(r.index) * unit;
-    r.valid = (r.index < 0 || at >= r.seq_len) ? 0 : static_cast<int>(min(static_cast<long long>(unit), r.seq_len - at));
+    r.valid = (r.index < 0 || at >= r.seq_len || r.seq_len <= p.steps) ? 0 : static_cast<int>(min(static_cast<long long>(unit), r.seq_len - at));
     r.first = r.seq_first + static_cast<int>(r.valid ? at : 0);
     return r;
+}
+
+// The rows of a chunk slot, as the gates' kernel found them.
+struct Rows {
+    int first, valid;
+};
+__device__ __forceinline__ Rows slot_rows(const Params& p, int slot) {
+    const int2 r = p.rows[slot];
+    return Rows{r.x, r.y};
 }
 
 // ---------------------------------------------------------------------------

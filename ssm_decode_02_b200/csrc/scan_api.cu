@@ -11,8 +11,12 @@ namespace scan {
 namespace {
 
 constexpr int64_t kMaxTokens = (1LL << 31) - (1LL << 17);
-// Longest sequences (equal lengths) that the token-by-token kernel takes.
-constexpr int kStepTokens = 4;
+// Longest sequences that the token-by-token kernel takes.  Its time grows with the
+// tokens, that of the chunk kernels is the same for 1 and 128: 128 sequences, 80 heads
+// of 128 x 64, 111, 349 and 635 us for 1, 8 and 16 tokens against 570 to 820; 4
+// sequences 4.9, 15 and 27 us against 44; 16 of 16 heads of 128 x 128 6.8, 22 and 40
+// against 43.
+constexpr int kStepTokens = 12;
 
 bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128 || d == 256; }
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -53,6 +57,7 @@ size_t layout(const rsq_scan_config& c, bool backward, Params* p, uint8_t* base)
     p->tokens = static_cast<int>(c.tokens);
     p->len = c.ragged ? 0 : static_cast<int>(c.tokens / c.sequences);
     auto slots_of = [&](int unit) {
+        if (!c.tokens) return 0;
         return c.ragged ? p->tokens / unit + p->n : p->n * ((p->len + unit - 1) / unit);
     };
     p->slots = slots_of(kChunk);
@@ -62,7 +67,8 @@ size_t layout(const rsq_scan_config& c, bool backward, Params* p, uint8_t* base)
     const bool tc = states_tc_ok(*p);
     const long long blocks = static_cast<long long>(p->n) * (backward ? 2 : 1) *
                              (tc ? p->H * p->P / 128 * std::max(1, p->N / 128) : p->H * p->tiles);
-    const int chunks = p->slots / p->n, fit = (tc ? 1 : 2) * kSms;
+    const int chunks = p->slots / p->n;
+    const int fit = (tc ? 1 : 2) * kSms;
     p->seg_chunks = 0;
     if (blocks * 4 <= fit && chunks >= 16) {
         const int want = static_cast<int>(fit / blocks);
@@ -80,6 +86,7 @@ size_t layout(const rsq_scan_config& c, bool backward, Params* p, uint8_t* base)
     const size_t cells = static_cast<size_t>(p->slots) * p->H;
     const size_t state = static_cast<size_t>(p->N) * kTile * p->tiles;
     p->flag = reinterpret_cast<unsigned*>(take(sizeof(unsigned)));
+    p->rows = reinterpret_cast<int2*>(take(static_cast<size_t>(p->slots) * sizeof(int2)));
     p->gb = reinterpret_cast<float2*>(take(cells * kChunk * sizeof(float2)));
     p->gdt = reinterpret_cast<float*>(take(cells * kChunk * sizeof(float)));
     if (backward) {
@@ -144,7 +151,8 @@ rsq_status check_workspace(const char* who, size_t need, const void* ws, size_t 
 // unit (keys, scores) is worth in quarters of a head's tile -- two tiles where a block
 // has one unit, little where the next one's beginning is hidden behind the last heads.
 int head_set(const Params& p, int start) {
-    const long long chunks = std::max(1, p.tokens / kChunk);
+    // of a ragged batch about half of the sequences' last chunks come on top
+    const long long chunks = std::max(1, std::min(p.slots, p.tokens / kChunk + (p.ragged ? p.n / 2 : 0)));
     int best = p.per;
     long long least = -1;
     for (int set = p.per; set >= 1; --set) {
@@ -237,10 +245,12 @@ rsq_status rsq_scan(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs, c
     p.out = static_cast<bf16*>(out);
     auto s = static_cast<cudaStream_t>(stream);
     if (steps) return done("scan", launch_step(p, s));
-    tc::Maps m;
+    p.steps = cfg->ragged ? kStepTokens : 0;
+    tc::Maps m{};
     int err = maps_for(p, false, &m);
-    if (!err && p.slots) err = launch_gates(p, s);
+    if (!err) err = p.slots ? launch_gates(p, s) : cudaMemsetAsync(p.flag, 0, sizeof(unsigned), s);
     if (!err) err = launch_states(p, m, false, s);
+    if (!err && p.steps) err = launch_step(p, s);
     if (!err && p.slots) err = launch_out(p, m, head_set(p, out_tc_ok(p) ? 1 : 8), s);
     return done("scan", err);
 }
@@ -286,9 +296,9 @@ rsq_status rsq_scan_backward(const rsq_scan_config* cfg, const rsq_scan_inputs* 
     p.dD = grads->dD;
     p.dstate_in = grads->dstate_in;
     auto s = static_cast<cudaStream_t>(stream);
-    tc::Maps m;
+    tc::Maps m{};
     int err = maps_for(p, true, &m);
-    if (!err && p.slots) err = launch_gates(p, s);
+    if (!err) err = p.slots ? launch_gates(p, s) : cudaMemsetAsync(p.flag, 0, sizeof(unsigned), s);
     if (!err) err = launch_states(p, m, true, s);
     if (!err) err = launch_backward(p, m, head_set(p, 8), s);
     return done("scan_backward", err);

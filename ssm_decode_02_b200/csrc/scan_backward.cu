@@ -75,7 +75,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__ Params p, int head_set) {
     using Sh = DxShape<N>;
     extern __shared__ __align__(128) uint8_t smem[];
-    const Range rg = slot_range(p, blockIdx.x, kChunk);
+    const Rows rg = slot_rows(p, blockIdx.x);
     const int sets = (p.per + head_set - 1) / head_set;
     const int group = blockIdx.y / sets, set = blockIdx.y - group * sets;
     const int h0 = group * p.per + set * head_set;
@@ -390,7 +390,7 @@ __device__ __forceinline__ void dk_body(const Params& p) {
     using Sh = DkShape<N>;
     constexpr int W = Sh::kW, NB = W / 8;
     extern __shared__ __align__(128) uint8_t smem[];
-    const Range rg = slot_range(p, blockIdx.x, kChunk);
+    const Rows rg = slot_rows(p, blockIdx.x);
     if (!rg.valid) return;
     const int parts = N / W, group = blockIdx.y / parts, n0 = (blockIdx.y - group * parts) * W;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;

@@ -28,7 +28,7 @@ constexpr int kSmem = 1024 + kStages * 2 * kX + kUnits * kUnit + kRaws * kRaw + 
 
 __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ tc::Maps maps) {
     extern __shared__ uint8_t raw_smem[];
-    const Range rg = slot_range(p, blockIdx.x, kChunk);
+    const Rows rg = slot_rows(p, blockIdx.x);
     if (!rg.valid) return;
     const int parts = p.N / 64, group = blockIdx.y / parts, n0 = (blockIdx.y - group * parts) * 64;
     const int h0 = group * p.per, heads = p.per, items = heads * p.tiles;

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                                                            int head_set) {
     using Sh = Shape<N>;
     extern __shared__ uint8_t raw_smem[];
-    const Range rg = slot_range(p, blockIdx.x, kChunk);
+    const Rows rg = slot_rows(p, blockIdx.x);
     const int sets = (p.per + head_set - 1) / head_set;
     const int group = blockIdx.y / sets, set = blockIdx.y - group * sets;
     const int h0 = group * p.per + set * head_set;

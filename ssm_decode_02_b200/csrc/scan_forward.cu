@@ -18,6 +18,7 @@ __global__ void __launch_bounds__(kThreads) gates_kernel(const __grid_constant__
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.flag = 0u;
     const int h = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5);
     const Range r = slot_range(p, slot, kChunk);
+    if (blockIdx.y == 0 && threadIdx.x == 0) p.rows[slot] = make_int2(r.first, r.valid);
     if (h >= p.H || !r.valid) return;
     double b[4];
     float dt[4];
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const __grid_constant_
     int seq, lo, len, slot0, seg_first = 1, seg_last = 1;
     if (p.seg_chunks) {
         const Range r = slot_range(p, blockIdx.x, kChunk * p.seg_chunks);
-        if (!r.valid && !(r.index == 0 && !ps.local)) return;
+        if (!r.valid && (p.steps || ps.local || r.index != 0)) return;   // of no rows, only a first one has a state to pass on
         seq = r.seq;
         lo = r.first;
         len = r.valid;
@@ -103,6 +104,7 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const __grid_constant_
     } else {
         seq = blockIdx.x;
         sequence(p, seq, lo, len);
+        if (p.steps && len <= p.steps) return;
         slot0 = first_slot(p, seq, lo, kChunk);
     }
     const int chunks = (len + kChunk - 1) / kChunk;
@@ -303,7 +305,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, N <= 128 ? 2 : 1) out_kernel(const __grid_constant__ Params p, int head_set) {
     using Sh = OutShape<N>;
     extern __shared__ __align__(128) uint8_t smem[];
-    const Range rg = slot_range(p, blockIdx.x, kChunk);
+    const Rows rg = slot_rows(p, blockIdx.x);
     if (!rg.valid) return;
     const int sets = (p.per + head_set - 1) / head_set;
     const int group = blockIdx.y / sets, set = blockIdx.y - group * sets;
@@ -473,6 +475,9 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
     __shared__ float4 part[kThreads / 32][16];
     const int tile = blockIdx.x % p.tiles, h = (blockIdx.x / p.tiles) % p.H;
     const int seq = blockIdx.x / p.tiles / p.H;
+    int lo, len;
+    sequence(p, seq, lo, len);
+    if (p.ragged && len > p.steps) return;   // the chunk kernels'
     const int cols = min(kTile, p.P - tile * kTile), groups = cols / 4, lanes = kThreads / groups;
     const int cg = threadIdx.x % groups, rl = threadIdx.x / groups, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long at = ((static_cast<long long>(seq) * p.H + h) * N) * p.P + tile * kTile + cg * 4;
@@ -484,8 +489,8 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
         if (p.state_in && row < N) S[r] = *reinterpret_cast<const float4*>(p.state_in + at + static_cast<long long>(row) * p.P);
     }
     const int group = h / p.per;
-    for (int t = 0; t < p.len; ++t) {
-        const long long tok = static_cast<long long>(seq) * p.len + t;
+    for (int t = 0; t < len; ++t) {
+        const long long tok = lo + t;
         for (int i = threadIdx.x; i < 2 * N; i += kThreads) {
             const bf16* src = i < N ? p.Bm + tok * p.bs + group * N + i : p.Cm + tok * p.cs + group * N + i - N;
             key[i / N][i % N] = __bfloat162float(*src);

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant
     auto unit_at = [&](int u, Unit& o) {
         const int per_slot = p.G * sets, y = u % per_slot;
         o.slot = u / per_slot;
-        const Range rg = slot_range(p, o.slot, kChunk);
+        const Rows rg = slot_rows(p, o.slot);
         o.first = rg.first;
         o.valid = rg.valid;
         o.group = y / sets;

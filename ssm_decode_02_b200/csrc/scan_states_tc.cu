@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
     int seq, lo, len, slot0, seg_first = 1, seg_last = 1;
     if (p.seg_chunks) {
         const Range r = slot_range(p, blockIdx.x, kChunk * p.seg_chunks);
-        if (!r.valid && !(r.index == 0 && !ps.local)) return;
+        if (!r.valid && (p.steps || ps.local || r.index != 0)) return;   // of no rows, only a first one has a state to pass on
         seq = r.seq;
         lo = r.first;
         len = r.valid;
@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
     } else {
         seq = blockIdx.x;
         sequence(p, seq, lo, len);
+        if (p.steps && len <= p.steps) return;
         slot0 = first_slot(p, seq, lo, kChunk);
     }
     const int chunks = (len + kChunk - 1) / kChunk, steps = 2 * chunks;

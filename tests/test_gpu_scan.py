@@ -90,6 +90,7 @@ EQUAL = [  # n, tokens, H, N, P, G
     (1, 1, 2, 16, 16, 1), (3, 3, 4, 128, 64, 1), (2, 4, 3, 256, 256, 3), (2, 8, 2, 64, 32, 2), (2, 10, 2, 32, 16, 1),
     (1, 127, 2, 128, 64, 1), (2, 256, 4, 64, 128, 2), (1, 129, 3, 16, 256, 3), (1, 300, 2, 256, 64, 1),
     (3, 3 * 65, 2, 32, 16, 2), (1, 513, 5, 128, 64, 1), (1, 200, 2, 128, 32, 1),
+    (1, 300, 2, 64, 256, 1), (2, 280, 2, 256, 256, 2), (1, 260, 2, 256, 128, 1), (1, 384, 4, 128, 128, 4), (5, 5 * 20, 2, 64, 64, 2),
 ]
 
 
@@ -100,7 +101,7 @@ def test_forward_equal_lengths(n, tokens, H, N, P, G, decay):
     check_forward(d, bounds, *forward(d, bounds, False, n))
 
 
-RAGGED = [([0, 1], 1), ([0, 0, 5, 5, 140, 269], 269), ([3, 3, 131, 259, 300], 310), ([0, 130, 131, 131], 140)]
+RAGGED = [([0, 1], 1), ([0, 12, 25, 25, 26, 300], 300), ([0, 0, 5, 5, 140, 269], 269), ([3, 3, 131, 259, 300], 310), ([0, 130, 131, 131], 140)]
 
 
 @pytest.mark.parametrize("bounds,tokens", RAGGED)
@@ -124,10 +125,19 @@ def test_forward_long_sequence_in_segments():
     check_forward(d, bounds, *forward(d, bounds, False, 1))
 
 
-def test_segments_of_a_ragged_batch():
-    bounds = [0, 0, 2100, 2101, 5000]
-    d, bounds = make(4, 5003, 1, 16, 16, 1, bounds=bounds, seed=9)
+@pytest.mark.parametrize("H,N,P", [(1, 16, 16), (2, 64, 64), (1, 128, 128)])
+def test_segments_of_a_ragged_batch(H, N, P):
+    bounds = [0, 0, 2100, 2101, 5000] if N == 16 else [0, 0, 4500, 4501, 4700]
+    total = bounds[-1] + 3
+    d, bounds = make(4, total, H, N, P, 1, bounds=bounds, seed=9)
     check_forward(d, bounds, *forward(d, bounds, True, 4))
+
+
+def test_growing_states():
+    """Decays above one: a state that grows."""
+    d, bounds = make(1, 300, 2, 64, 64, 1, decay=True, seed=15)
+    d["decay"] = 1 + 0.04 * (d["decay"] - 0.5)
+    check_forward(d, bounds, *forward(d, bounds, False, 1))
 
 
 def test_prompt_in_pieces_equals_the_prompt():
@@ -162,16 +172,22 @@ def test_token_rows_may_lie_apart():
     check_forward(d, bounds, out.cpu(), state.cpu())
 
 
-def test_no_tokens_keeps_the_state():
-    c = torch.randn(2, 2, 16, 16, device="cuda")
+@pytest.mark.parametrize("N", [16, 64])
+def test_no_tokens_keeps_the_state(N):
+    c = torch.randn(2, 2, N, 64, device="cuda")
     for ragged in (False, True):
-        s = rsq.Scan(2, 0, 2, 16, 16, ragged=ragged)
+        s = rsq.Scan(2, 0, 2, N, 64, ragged=ragged)
         state = torch.empty_like(c)
         ones = torch.ones(4, device="cuda")
         cu = torch.zeros(3, dtype=torch.int32, device="cuda") if ragged else None
-        s.forward(rsq.scan_inputs(None, None, None, ones, ones), None, state_in=c, state_out=state, cu_seqlens=cu,
-                  workspace=s.alloc_workspace())
+        none = rsq.scan_inputs(None, None, None, ones, ones)
+        s.forward(none, None, state_in=c, state_out=state, cu_seqlens=cu, workspace=poison(s.alloc_workspace()))
         assert torch.equal(state, c)
+        dA, dS = torch.full((2,), 5.0, device="cuda"), torch.empty_like(c)
+        ws = poison(s.alloc_workspace(True))
+        s.backward(none, None, rsq.scan_grads(dA=dA, dstate_in=dS), dstate_out=c, cu_seqlens=cu, workspace=ws)
+        rsq.rsq_scan_check(ws)
+        assert torch.equal(dS, c) and (dA == 0).all()
 
 
 def test_nan_stays_in_its_sequence_and_behind_bad_bounds_nothing_moves():
@@ -245,7 +261,8 @@ def check_backward(d, bounds, got, want):
 
 
 BACK = [(1, 1, 2, 16, 16, 1), (2, 256, 4, 64, 64, 2), (1, 129, 3, 128, 64, 1), (1, 140, 2, 256, 128, 2), (2, 60, 3, 32, 256, 1),
-        (1, 400, 2, 16, 32, 2), (3, 3 * 131, 2, 128, 128, 1)]
+        (1, 400, 2, 16, 32, 2), (3, 3 * 131, 2, 128, 128, 1), (1, 200, 2, 64, 256, 1), (1, 256, 2, 256, 256, 2), (1, 256, 4, 128, 128, 4),
+        (2, 2 * 70, 6, 64, 64, 2)]
 
 
 @pytest.mark.parametrize("n,tokens,H,N,P,G", BACK)
@@ -278,10 +295,11 @@ def test_backward_strong_decays_and_restarts(decay):
         assert (got["dlog_decay"][d["decay"] == 0] == 0).all()
 
 
-def test_backward_long_sequence_in_segments():
-    d, bounds = make(1, 128 * 33 + 5, 1, 16, 16, 1, seed=8)
+@pytest.mark.parametrize("T,H,N,P", [(128 * 33 + 5, 1, 16, 16), (128 * 18 + 70, 2, 64, 64)])
+def test_backward_long_sequence_in_segments(T, H, N, P):
+    d, bounds = make(1, T, H, N, P, 1, seed=8)
     g = torch.Generator().manual_seed(4)
-    dout, dstate = torch.randn(d["x"].shape, generator=g).bfloat16(), torch.randn((1, 1, 16, 16), generator=g)
+    dout, dstate = torch.randn(d["x"].shape, generator=g).bfloat16(), torch.randn((1, H, N, P), generator=g)
     check_backward(d, bounds, backward(d, bounds, False, 1, dout, dstate), reference_grads(d, bounds, dout, dstate))
 
 
