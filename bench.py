@@ -776,7 +776,8 @@ def run_prompt(args, w: W.Workload) -> int:
     bits = np.asarray(head_bits_of(w, rsq), np.int8)
     ctx = rsq.Context(rsq.RSQ_MAMBA2, B, H, N, P, head_bits=bits, rounding=ROUNDING[w.rounding], seed=w.sr_seed, ngroups=G)
     stored = ctx.alloc_state(dev)
-    step_ins = rsq.mamba2_inputs(x[:B].clone(), Bm[:B].clone(), Cm[:B].clone(), dt[:B].clone(), A, D)
+    token = [t[:B].clone() for t in (x, Bm, Cm, dt)]     # mamba2_inputs holds addresses: these live until the end
+    step_ins = rsq.mamba2_inputs(*token, A, D)
     step_out, step_z = torch.empty((B, H, P), dtype=f32, device=dev), z[:B].clone()
     step_y = torch.empty_like(step_z)
     step_norm = rsq.norm_config(step_out.view(B, width), step_z, torch.bfloat16, order=rsq.RSQ_GATE_NORM)
@@ -808,6 +809,7 @@ def run_prompt(args, w: W.Workload) -> int:
     rsq.rsq_scan_check(ws)
     decode_ms = timed(decode, 4 * steps)
     flags = ctx.check_flags()
+    del token
     emit({"metric": "prompt_tokens_per_s", "value": tokens / prompt_ms * 1e3, "unit": "tokens/s", "n_gpus": 1, "steps": steps,
           "warmup": max(3, min(args.warmup, 10)), "ms_per_step": prompt_ms, "decode_ms_per_token": decode_ms, "flags": flags,
           "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",

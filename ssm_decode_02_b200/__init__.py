@@ -224,6 +224,28 @@ def _workspace(t) -> tuple[int | None, int]:
     return _dptr(t), t.numel() * t.element_size()
 
 
+def _current_device() -> int:
+    global _current_device
+    import torch
+    torch.cuda.current_device()
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
+
+
+def _sized(count: int, item: int, **tensors) -> None:
+    """Refuses tensors of fewer than count elements, or of elements of other than item bytes:
+    the kernels take their sizes from the configuration alone."""
+    for name, t in tensors.items():
+        if t is not None and not isinstance(t, int) and (t.numel() < count or t.element_size() != item):
+            raise ValueError("%s: expected at least %d elements of %d bytes, got %s of %s" % (name, count, item, tuple(t.shape), t.dtype))
+
+
+def _here(t) -> None:
+    """Refuses a tensor of another GPU than the current one, whose stream the call uses."""
+    if t is not None and not isinstance(t, int) and t.is_cuda and t.get_device() != _current_device():
+        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (t.get_device(), _current_device()))
+
+
 def _dtype_of(t) -> int:
     """rsq_dtype of a tensor or a torch dtype."""
     import torch
@@ -489,13 +511,37 @@ def rsq_norm_workspace(cfg: rsq_norm_config) -> int:
     return int(n.value)
 
 
+_ITEM = {RSQ_F32: 4, RSQ_BF16: 2}
+
+
+def _norm_sized(cfg, x, side, y, w) -> None:
+    """As _sized and _here for what every norm call has, written out: a decode step's call
+    takes a few microseconds in all."""
+    n = cfg.rows * cfg.width
+    try:
+        if (y.numel() < n or w.numel() < cfg.width
+                or (x is not None and (x.numel() < n or x.element_size() != _ITEM[cfg.x_dtype]))
+                or y.element_size() != _ITEM[cfg.y_dtype] or w.element_size() != 4
+                or (side is not None and (side.numel() < n or side.element_size() != _ITEM[cfg.side_dtype]))):
+            raise ValueError("expected %d rows of %d columns in the configuration's types, got %s"
+                             % (cfg.rows, cfg.width, [(tuple(t.shape), t.dtype) for t in (x, side, y, w) if t is not None]))
+        _here(y)
+    except AttributeError:      # addresses
+        pass
+
+
 def rsq_gated_norm(cfg: rsq_norm_config, x, z, w, y, stream=None) -> None:
     """x and z may be row-strided (norm_config reads their strides)."""
+    _norm_sized(cfg, x, z, y, w)
     _check(lib.rsq_gated_norm(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(z), _dptr(w), _dptr(y),
                               _stream(stream)))
 
 
 def rsq_gated_norm_backward(cfg: rsq_norm_config, x, z, w, dy, dx, dz, dw, workspace=None, stream=None) -> None:
+    _norm_sized(cfg, x, z, dy, w)
+    _sized(cfg.rows * cfg.width, _ITEM.get(cfg.x_dtype, 0), dx=dx)
+    _sized(cfg.rows * cfg.width, _ITEM.get(cfg.side_dtype, 0), dz=dz)
+    _sized(cfg.width, 4, dw=dw)
     ws, n = _workspace(workspace)
     _check(lib.rsq_gated_norm_backward(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(z), _dptr(w), _dptr(dy),
                                        _dptr(dx), _dptr(dz), _dptr(dw), ws, n, _stream(stream)))
@@ -503,12 +549,21 @@ def rsq_gated_norm_backward(cfg: rsq_norm_config, x, z, w, dy, dx, dz, dw, works
 
 def rsq_residual_norm(cfg: rsq_norm_config, x, residual, scale, w, h, y, stream=None) -> None:
     """x and residual may be row-strided (norm_config reads their strides)."""
+    _norm_sized(cfg, x, residual, y, w)
+    if h is not residual:
+        _sized(cfg.rows * cfg.width, _ITEM.get(cfg.side_dtype, 0), h=h)
+    if scale is not None:
+        _sized(cfg.width, 4, scale=scale)
     _check(lib.rsq_residual_norm(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(residual), _dptr(scale), _dptr(w),
                                  _dptr(h), _dptr(y), _stream(stream)))
 
 
 def rsq_residual_norm_backward(cfg: rsq_norm_config, x, h, scale, w, dy, dh, dx, dresidual, dscale, dw,
                                workspace=None, stream=None) -> None:
+    _norm_sized(cfg, x, h, dy, w)
+    _sized(cfg.rows * cfg.width, _ITEM.get(cfg.side_dtype, 0), dh=dh, dresidual=dresidual)
+    _sized(cfg.rows * cfg.width, _ITEM.get(cfg.x_dtype, 0), dx=dx)
+    _sized(cfg.width, 4, scale=scale, dw=dw, dscale=dscale)
     ws, n = _workspace(workspace)
     _check(lib.rsq_residual_norm_backward(ctypes.byref(cfg), _dptr_rows(x), _dptr(h), _dptr(scale), _dptr(w),
                                           _dptr(dy), _dptr(dh), _dptr(dx), _dptr(dresidual), _dptr(dscale),
@@ -566,15 +621,24 @@ def _token_rows(t, what: str) -> tuple[int | None, int]:
 
 
 def scan_inputs(x, Bm, Cm, dt=None, A=None, D=None, decay=None) -> rsq_scan_inputs:
-    """x [tokens, heads, dv], Bm, Cm [tokens, ngroups, dk]: their tokens may lie apart."""
+    """x [tokens, heads, dv], Bm, Cm [tokens, ngroups, dk]: their tokens may lie apart.  The
+    result keeps the tensors that it points at."""
     (xp, xs), (bp, bs), (cp, cs) = _token_rows(x, "x"), _token_rows(Bm, "Bm"), _token_rows(Cm, "Cm")
-    return rsq_scan_inputs(xp, bp, cp, _dptr(dt), _dptr(A), _dptr(D), _dptr(decay), xs, bs, cs)
+    for name, t, item in (("x", x, 2), ("Bm", Bm, 2), ("Cm", Cm, 2), ("dt", dt, 4), ("A", A, 4), ("D", D, 4), ("decay", decay, 4)):
+        if t is not None and not isinstance(t, int) and t.element_size() != item:
+            raise ValueError("%s: expected %s, got %s" % (name, "bfloat16" if item == 2 else "float32", t.dtype))
+    ins = rsq_scan_inputs(xp, bp, cp, _dptr(dt), _dptr(A), _dptr(D), _dptr(decay), xs, bs, cs)
+    ins.tensors = (x, Bm, Cm, dt, A, D, decay)
+    return ins
 
 
 def scan_grads(dx=None, dBm=None, dCm=None, ddt=None, dlog_decay=None, dA=None, dD=None,
                dstate_in=None) -> rsq_scan_grads:
-    return rsq_scan_grads(_dptr(dx), _dptr(dBm), _dptr(dCm), _dptr(ddt), _dptr(dlog_decay), _dptr(dA),
-                          _dptr(dD), _dptr(dstate_in))
+    """Null for a gradient that is not wanted.  The result keeps the tensors that it points at."""
+    grads = rsq_scan_grads(_dptr(dx), _dptr(dBm), _dptr(dCm), _dptr(ddt), _dptr(dlog_decay), _dptr(dA),
+                           _dptr(dD), _dptr(dstate_in))
+    grads.tensors = (dx, dBm, dCm, ddt, dlog_decay, dA, dD, dstate_in)
+    return grads
 
 
 def norm_config(x, side, y, *, group: int = 0, order: int = RSQ_NORM_GATE, eps: float = 1e-5) -> rsq_norm_config:
@@ -607,12 +671,31 @@ class Scan:
         n = self.backward_workspace_bytes if backward else self.workspace_bytes
         return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
+    def _fits(self, inputs, cu_seqlens, grads=(None,) * 8, states=(), tokens=()):
+        """Sizes of the tensors behind a call's arguments (the kernels know the configuration's)."""
+        c = self.cfg
+        x, Bm, Cm, dt, A, D, decay = getattr(inputs, "tensors", (None,) * 7)
+        dx, dBm, dCm, ddt, dlog, dA, dD, dstate = grads
+        _here(x)
+        for name, t, row in (("x", x, c.heads * c.dv), ("Bm", Bm, c.ngroups * c.dk), ("Cm", Cm, c.ngroups * c.dk)):
+            if t is not None and not isinstance(t, int) and t.numel() != t.shape[0] * row:
+                raise ValueError("%s: expected %d elements a token, got %s" % (name, row, tuple(t.shape)))
+        _sized(c.tokens * c.heads * c.dv, 2, x=x, dx=dx, **{"out": t for t in tokens})
+        _sized(c.tokens * c.ngroups * c.dk, 2, Bm=Bm, Cm=Cm, dBm=dBm, dCm=dCm)
+        _sized(c.tokens * c.heads, 4, dt=dt, decay=decay, ddt=ddt, dlog_decay=dlog)
+        _sized(c.heads, 4, A=A, D=D, dA=dA, dD=dD)
+        for t in states + (dstate,):
+            _sized(c.sequences * c.heads * c.dk * c.dv, 4, state=t)
+        _sized(c.sequences + 1, 4, cu_seqlens=cu_seqlens)
+
     def forward(self, inputs, out, *, state_in=None, state_out=None, cu_seqlens=None, workspace=None, stream=None):
+        self._fits(inputs, cu_seqlens, states=(state_in, state_out), tokens=(out,))
         rsq_scan(self.cfg, inputs, out, cu_seqlens=cu_seqlens, state_in=state_in, state_out=state_out,
                  workspace=workspace, stream=stream)
 
     def backward(self, inputs, dout, grads, *, state_in=None, dstate_out=None, cu_seqlens=None, workspace=None,
                  stream=None):
+        self._fits(inputs, cu_seqlens, getattr(grads, "tensors", (None,) * 8), (state_in, dstate_out), (dout,))
         rsq_scan_backward(self.cfg, inputs, dout, grads, cu_seqlens=cu_seqlens, state_in=state_in,
                           dstate_out=dstate_out, workspace=workspace, stream=stream)
 

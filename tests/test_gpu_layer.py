@@ -228,8 +228,9 @@ def test_failure_mark_is_reported():
     rsq.rsq_scan_check(ws)
 
 
-def test_prompt_mode_of_the_bench():
-    r = subprocess.run([sys.executable, "bench.py", "--workload", "mamba2_b128_h80_p64_n128_int8_sr", "--prompt", "64", "--steps", "2",
+@pytest.mark.parametrize("tokens", [64, 512])
+def test_prompt_mode_of_the_bench(tokens):
+    r = subprocess.run([sys.executable, "bench.py", "--workload", "mamba2_b128_h80_p64_n128_int8_sr", "--prompt", str(tokens), "--steps", "10",
                         "--warmup", "3"], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     line = json.loads(r.stdout.strip().splitlines()[-1])

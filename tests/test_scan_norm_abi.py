@@ -142,3 +142,63 @@ def test_binding_refuses_tensors():
         rsq.norm_config(t.half(), None, torch.bfloat16)
     with pytest.raises(ValueError):
         rsq.rsq_gated_norm(_norm(), t, None, t, t, stream=0)
+
+
+class _On:
+    """What the binding reads of a CUDA tensor; its address is never followed."""
+
+    def __init__(self, *shape, dtype=torch.float32, device=0):
+        self.t, self.device = torch.empty(shape, dtype=dtype, device="meta"), device
+        self.is_cuda, self.shape, self.dtype = True, self.t.shape, dtype
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def data_ptr(self):
+        return P
+
+    def get_device(self):
+        return self.device
+
+
+def test_binding_refuses_sizes_and_types(monkeypatch):
+    monkeypatch.setattr(rsq, "_current_device", lambda: 0)
+    monkeypatch.setattr(rsq, "lib", None)                        # no call goes through
+    bf = torch.bfloat16
+    T, H, N, D = 256, 4, 64, 64
+    scan = rsq.Scan.__new__(rsq.Scan)
+    scan.cfg = rsq.rsq_scan_config(rsq.RSQ_MAMBA2, rsq.RSQ_BF16, 2, H, N, D, 1, 0, T)
+    good = dict(x=_On(T, H, D, dtype=bf), Bm=_On(T, 1, N, dtype=bf), Cm=_On(T, 1, N, dtype=bf), dt=_On(T, H), A=_On(H), D=_On(H))
+    out, state = _On(T, H, D, dtype=bf), _On(2, H, N, D)
+    for name, t in [("x", _On(T, H, D)), ("Bm", _On(T, 1, N)), ("dt", _On(T, H, dtype=bf)), ("A", _On(H, dtype=bf))]:
+        with pytest.raises(ValueError, match=name):
+            rsq.scan_inputs(**(good | {name: t}))
+    for name, t in [("x", _On(T - 1, H, D, dtype=bf)), ("Cm", _On(T, 2, N, dtype=bf)), ("dt", _On(T, 1)), ("D", _On(H - 1))]:
+        with pytest.raises(ValueError, match=name):
+            scan.forward(rsq.scan_inputs(**(good | {name: t})), out)
+    ins = rsq.scan_inputs(**good)
+    for kw in [dict(out=_On(T, H, D)), dict(state_in=_On(1, H, N, D)), dict(state_out=_On(2, H, N, D, dtype=bf)),
+               dict(cu_seqlens=_On(2, dtype=torch.int32)), dict(cu_seqlens=_On(3, dtype=torch.int64))]:
+        with pytest.raises(ValueError):
+            scan.forward(ins, **(dict(out=out) | kw))
+    for kw in [dict(dx=_On(T, H, D)), dict(dBm=_On(1, N, dtype=bf)), dict(ddt=_On(H)),
+               dict(dA=_On(1)), dict(dstate_in=_On(1, H, N, D))]:
+        with pytest.raises(ValueError):
+            scan.backward(ins, out, rsq.scan_grads(**kw))
+    with pytest.raises(ValueError, match="cuda:1"):
+        scan.forward(rsq.scan_inputs(**(good | {"x": _On(T, H, D, dtype=bf, device=1)})), out)
+    assert ins.tensors[0] is good["x"] and state.is_cuda
+
+    x, z, w = _On(4, 64, dtype=bf), _On(4, 64, dtype=bf), _On(64)
+    cfg = rsq.rsq_norm_config(4, 64, 0, 0, rsq.RSQ_BF16, rsq.RSQ_BF16, rsq.RSQ_BF16, 1e-5, 0, 0)
+    for a in [(_On(4, 64), z, w, x), (x, _On(3, 64, dtype=bf), w, x), (x, z, _On(63), x), (x, z, w, _On(4, 64)),
+              (x, z, w, _On(4, 64, dtype=bf, device=1))]:
+        with pytest.raises(ValueError):
+            rsq.rsq_gated_norm(cfg, *a)
+    for a in [(x, z, None, w, z, _On(4, 64)), (x, z, _On(1), w, z, x), (x, z, None, w, _On(4, 64), x)]:
+        with pytest.raises(ValueError):
+            rsq.rsq_residual_norm(cfg, *a)
+    with pytest.raises(ValueError):
+        rsq.rsq_gated_norm_backward(cfg, x, z, w, x, _On(4, 64), z, None)
+    with pytest.raises(ValueError):
+        rsq.rsq_residual_norm_backward(cfg, x, z, None, w, x, z, x, _On(4, 63, dtype=bf), None, None)
