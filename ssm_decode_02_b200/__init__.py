@@ -501,7 +501,10 @@ def rsq_scan_backward(cfg: rsq_scan_config, inputs: rsq_scan_inputs, dout, grads
 
 
 def rsq_scan_check(workspace, stream=None) -> None:
-    """Raises when a kernel of the last call with this workspace gave up a wait."""
+    """Raises when a kernel of the last call with this workspace gave up a wait.  None, the
+    workspace of calls that need none: nothing waits."""
+    if workspace is None:
+        return
     _check(lib.rsq_scan_check(_dptr(workspace), _stream(stream)))
 
 

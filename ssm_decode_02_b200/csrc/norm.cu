@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "rsq_internal.h"
+#include "scan_launch.cuh"
 
 namespace rsq {
 namespace {
@@ -293,6 +294,7 @@ constexpr bool kKeepCols = VEC * K <= 16;
 template <int MODE, class TX, class TS, class TY, int VEC, int K>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(VEC * K <= 16 && VEC == 8 ? kBackwardRegs : 128)
 norm_backward_kernel(const __grid_constant__ NormParams p) {
+    let_next();
     constexpr bool GATED = MODE == kNormGate || MODE == kGateNorm;
     constexpr bool KEEP = kKeepCols<VEC, K>;
     extern __shared__ float4 own4[];  // sums of dw, of dscale (if wanted), w, scale: [K][threads] vectors each
@@ -444,6 +446,7 @@ norm_backward_kernel(const __grid_constant__ NormParams p) {
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* part_w, const float* part_s, int parts, int width,
                                                           float* out_w, float* out_s) {
     __shared__ float sh[32][33];
+    wait_before();
     const float* part = blockIdx.y ? part_s : part_w;
     float* out = blockIdx.y ? out_s : out_w;
     if (!out) return;
@@ -595,8 +598,8 @@ rsq_status run_backward(const char* who, int mode, const rsq_norm_config& c, Nor
     }
     int err = launch(mode, true, c, p, g, s);
     if (!err && (dw || dscale)) {
-        column_sum_kernel<<<dim3((c.width + 31) / 32, dscale ? 2 : 1), 1024, 0, s>>>(p.part_w, p.part_s, g.gx, c.width, dw, dscale);
-        err = cudaGetLastError();
+        err = rsq::launch(column_sum_kernel, dim3((c.width + 31) / 32, dscale ? 2 : 1), 1024, 0, s, false, p.part_w, p.part_s, g.gx, c.width,
+                          dw, dscale);
     }
     return err ? set_error(RSQ_E_CUDA, "%s: %s", who, cudaGetErrorString(static_cast<cudaError_t>(err))) : RSQ_OK;
 }

@@ -19,6 +19,7 @@
 
 #include "rsq_device.cuh"
 #include "rsq_internal.h"
+#include "scan_launch.cuh"
 
 namespace rsq {
 namespace scan {

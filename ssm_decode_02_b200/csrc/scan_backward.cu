@@ -75,6 +75,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__ Params p, int head_set) {
     using Sh = DxShape<N>;
     extern __shared__ __align__(128) uint8_t smem[];
+    wait_before();
     const Rows rg = slot_rows(p, blockIdx.x);
     const int sets = (p.per + head_set - 1) / head_set;
     const int group = blockIdx.y / sets, set = blockIdx.y - group * sets;
@@ -516,6 +517,7 @@ __device__ __forceinline__ void dk_body(const Params& p) {
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) dk_kernel(const __grid_constant__ Params p) {
+    wait_before();
     if (blockIdx.z == 0) {
         if (p.dCm) dk_body<N, false>(p);
     } else {
@@ -526,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) dk_kernel(const __grid_constant__
 // dA, dD: sums of the chunks' parts, eight interleaved runs in order.
 __global__ void __launch_bounds__(256) sums_kernel(const __grid_constant__ Params p) {
     __shared__ float sh[8][33];
+    wait_before();
     const int h = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
     float* out = blockIdx.y ? p.dD : p.dA;
     if (!out) return;
@@ -551,21 +554,18 @@ int backward_n(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s)
         if (dx_tc_ok(p)) {
             err = launch_dx_tc(p, m, head_set, s);
         } else {
-            dx_kernel<N><<<grid, kThreads, DxShape<N>::kSmem, s>>>(p, head_set);
-            err = cudaGetLastError();
+            err = launch(dx_kernel<N>, grid, kThreads, DxShape<N>::kSmem, s, false, p, head_set);
         }
         if (!err && (p.dBm || p.dCm)) {
             if (dk_tc_ok(p)) {
                 err = launch_dk_tc(p, m, s);
             } else {
-                dk_kernel<N><<<dim3(p.slots, p.G * (N / DkShape<N>::kW), 2), kThreads, DkShape<N>::kSmem, s>>>(p);
-                err = cudaGetLastError();
+                err = launch(dk_kernel<N>, dim3(p.slots, p.G * (N / DkShape<N>::kW), 2), kThreads, DkShape<N>::kSmem, s, false, p);
             }
         }
         if (err) return err;
     }
-    if (p.dA || p.dD) sums_kernel<<<dim3((p.H + 31) / 32, 2), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return p.dA || p.dD ? launch(sums_kernel, dim3((p.H + 31) / 32, 2), 256, 0, s, false, p) : 0;
 }
 
 }  // namespace

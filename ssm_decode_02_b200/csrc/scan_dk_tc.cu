@@ -28,6 +28,7 @@ constexpr int kSmem = 1024 + kStages * 2 * kX + kUnits * kUnit + kRaws * kRaw + 
 
 __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant__ Params p, const __grid_constant__ tc::Maps maps) {
     extern __shared__ uint8_t raw_smem[];
+    wait_before();
     const Rows rg = slot_rows(p, blockIdx.x);
     if (!rg.valid) return;
     const int parts = p.N / 64, group = blockIdx.y / parts, n0 = (blockIdx.y - group * parts) * 64;
@@ -393,8 +394,7 @@ __global__ void __launch_bounds__(kBlock, 1) dk_tc_kernel(const __grid_constant_
 int launch_dk_tc(const Params& p, const tc::Maps& m, cudaStream_t s) {
     const int err = cudaFuncSetAttribute(dk_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (err) return err;
-    dk_tc_kernel<<<dim3(p.slots, p.G * (p.N / 64)), kBlock, kSmem, s>>>(p, m);
-    return cudaGetLastError();
+    return launch(dk_tc_kernel, dim3(p.slots, p.G * (p.N / 64)), kBlock, kSmem, s, false, p, m);
 }
 
 }  // namespace scan

@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                                                            int head_set) {
     using Sh = Shape<N>;
     extern __shared__ uint8_t raw_smem[];
+    wait_before();
     const Rows rg = slot_rows(p, blockIdx.x);
     const int sets = (p.per + head_set - 1) / head_set;
     const int group = blockIdx.y / sets, set = blockIdx.y - group * sets;
@@ -563,8 +564,7 @@ int run(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s) {
     const int err = cudaFuncSetAttribute(dx_tc_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<N>::kSmem);
     if (err) return err;
     const dim3 grid(p.slots, p.G * ((p.per + head_set - 1) / head_set));
-    dx_tc_kernel<N><<<grid, kBlock, Shape<N>::kSmem, s>>>(p, m, head_set);
-    return cudaGetLastError();
+    return launch(dx_tc_kernel<N>, grid, kBlock, Shape<N>::kSmem, s, false, p, m, head_set);
 }
 
 }  // namespace

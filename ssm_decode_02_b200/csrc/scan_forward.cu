@@ -13,13 +13,29 @@ namespace {
 // strong decays and behind a decay of zero.  Rows past the end of the sequence
 // have a_t = 1 and dt = 0.
 // ---------------------------------------------------------------------------
+constexpr int kGateHeads = kThreads / 32;   // of a block
+
 __global__ void __launch_bounds__(kThreads) gates_kernel(const __grid_constant__ Params p) {
-    const int slot = blockIdx.x, lane = threadIdx.x & 31;
+    let_next();
+    // the heads' values of a token lie side by side: read so, and turned here
+    __shared__ __align__(16) float sdt[kGateHeads][kChunk + 4], sa[kGateHeads][kChunk + 4];
+    const int slot = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.flag = 0u;
-    const int h = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5);
+    const int h0 = blockIdx.y * kGateHeads, h = h0 + warp;
     const Range r = slot_range(p, slot, kChunk);
     if (blockIdx.y == 0 && threadIdx.x == 0) p.rows[slot] = make_int2(r.first, r.valid);
-    if (h >= p.H || !r.valid) return;
+    if (!r.valid) return;
+#pragma unroll
+    for (int i = threadIdx.x; i < kChunk * kGateHeads; i += kThreads) {
+        const int t = i / kGateHeads, k = i % kGateHeads;
+        if (t < r.valid && h0 + k < p.H) {
+            const long long at = static_cast<long long>(r.first + t) * p.H + h0 + k;
+            if (p.dt) sdt[k][t] = __ldg(p.dt + at);
+            if (p.decay) sa[k][t] = __ldg(p.decay + at);
+        }
+    }
+    __syncthreads();
+    if (h >= p.H) return;
     double b[4];
     float dt[4];
 #pragma unroll
@@ -28,10 +44,9 @@ __global__ void __launch_bounds__(kThreads) gates_kernel(const __grid_constant__
         b[i] = 0.;
         dt[i] = 0.f;
         if (t < r.valid) {
-            const long long at = static_cast<long long>(r.first + t) * p.H + h;
-            dt[i] = p.dt ? __ldg(p.dt + at) : 1.f;
+            dt[i] = p.dt ? sdt[warp][t] : 1.f;
             if (p.decay) {
-                const float a = __ldg(p.decay + at);
+                const float a = sa[warp][t];
                 b[i] = a == 0.f ? kLogZero : static_cast<double>(log2f(a));
             } else {
                 b[i] = static_cast<double>(dt[i]) * static_cast<double>(__ldg(p.A + h)) * 1.4426950408889634;
@@ -85,6 +100,7 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const __grid_constant_
                                                           const __grid_constant__ Pass bwd) {
     using Sh = StateShape<N>;
     extern __shared__ __align__(128) uint8_t smem[];
+    wait_before();
     const Pass& ps = blockIdx.z ? bwd : fwd;
     const int h = blockIdx.y / p.tiles, tile = blockIdx.y - h * p.tiles;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -259,6 +275,8 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const __grid_constant_
 __global__ void __launch_bounds__(kThreads) segments_kernel(const __grid_constant__ Params p,
                                                             const __grid_constant__ Pass fwd,
                                                             const __grid_constant__ Pass bwd) {
+    wait_before();
+    let_next();
     const bool rev = blockIdx.z & 1;
     const Pass& ps = rev ? bwd : fwd;
     const int seq = blockIdx.z >> 1, h = blockIdx.y;
@@ -267,6 +285,7 @@ __global__ void __launch_bounds__(kThreads) segments_kernel(const __grid_constan
     if (!ps.k || e >= cells) return;
     int lo, len;
     sequence(p, seq, lo, len);
+    if (p.steps && len <= p.steps) return;
     const int unit = kChunk * p.seg_chunks;
     const int slot0 = first_slot(p, seq, lo, unit), segs = max(1, (len + unit - 1) / unit);
     float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -305,6 +324,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, N <= 128 ? 2 : 1) out_kernel(const __grid_constant__ Params p, int head_set) {
     using Sh = OutShape<N>;
     extern __shared__ __align__(128) uint8_t smem[];
+    wait_before();
     const Rows rg = slot_rows(p, blockIdx.x);
     if (!rg.valid) return;
     const int sets = (p.per + head_set - 1) / head_set;
@@ -473,6 +493,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
     constexpr int R = N / 16;                    // rows of a thread at 64 columns
     __shared__ float key[2][N];                  // B, C of the token
     __shared__ float4 part[kThreads / 32][16];
+    wait_before();
     const int tile = blockIdx.x % p.tiles, h = (blockIdx.x / p.tiles) % p.H;
     const int seq = blockIdx.x / p.tiles / p.H;
     int lo, len;
@@ -540,11 +561,12 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
                 make_uint2(pack(y.x, y.y), pack(y.z, y.w));
         }
     }
-    if (!p.state_out) return;
+    if (p.state_out) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int row = rl + r * lanes;
-        if (row < N) *reinterpret_cast<float4*>(p.state_out + at + static_cast<long long>(row) * p.P) = S[r];
+        for (int r = 0; r < R; ++r) {
+            const int row = rl + r * lanes;
+            if (row < N) *reinterpret_cast<float4*>(p.state_out + at + static_cast<long long>(row) * p.P) = S[r];
+        }
     }
 }
 
@@ -561,8 +583,7 @@ int states_n(const Params& p, const tc::Maps& m, bool backward, const Pass& f, c
     auto* k = backward ? states_kernel<N, true> : states_kernel<N, false>;
     const int err = allow_smem(k, Sh::kSmem);
     if (err) return err;
-    k<<<grid, kThreads, Sh::kSmem, s>>>(p, f, b);
-    return cudaGetLastError();
+    return launch(k, grid, kThreads, Sh::kSmem, s, !p.slots, p, f, b);
 }
 
 int states_pass(const Params& p, const tc::Maps& m, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
@@ -581,15 +602,13 @@ int out_n(const Params& p, int head_set, cudaStream_t s) {
     const int err = allow_smem(out_kernel<N>, Sh::kSmem);
     if (err) return err;
     const dim3 grid(p.slots, p.G * ((p.per + head_set - 1) / head_set));
-    out_kernel<N><<<grid, kThreads, Sh::kSmem, s>>>(p, head_set);
-    return cudaGetLastError();
+    return launch(out_kernel<N>, grid, kThreads, Sh::kSmem, s, false, p, head_set);
 }
 
 }  // namespace
 
 int launch_gates(const Params& p, cudaStream_t s) {
-    gates_kernel<<<dim3(p.slots, (p.H + 7) / 8), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch(gates_kernel, dim3(p.slots, (p.H + kGateHeads - 1) / kGateHeads), kThreads, 0, s, true, p);
 }
 
 int launch_states(const Params& p, const tc::Maps& m, bool backward, cudaStream_t s) {
@@ -600,22 +619,22 @@ int launch_states(const Params& p, const tc::Maps& m, bool backward, cudaStream_
         lf.local = lb.local = 1;
         int err = states_pass(p, m, backward, lf, lb, s);
         if (err) return err;
-        segments_kernel<<<dim3((p.N * p.P / 4 + kThreads - 1) / kThreads, p.H, 2 * p.n), kThreads, 0, s>>>(p, f, b);
-        if ((err = cudaGetLastError())) return err;
+        err = launch(segments_kernel, dim3((p.N * p.P / 4 + kThreads - 1) / kThreads, p.H, 2 * p.n), kThreads, 0, s, false, p, f, b);
+        if (err) return err;
     }
     return states_pass(p, m, backward, f, b, s);
 }
 
 int launch_step(const Params& p, cudaStream_t s) {
     const unsigned grid = static_cast<unsigned>(p.n) * p.H * p.tiles;
+    const bool first = !p.ragged;
     switch (p.N) {
-        case 16: step_kernel<16><<<grid, kThreads, 0, s>>>(p); break;
-        case 32: step_kernel<32><<<grid, kThreads, 0, s>>>(p); break;
-        case 64: step_kernel<64><<<grid, kThreads, 0, s>>>(p); break;
-        case 128: step_kernel<128><<<grid, kThreads, 0, s>>>(p); break;
-        default: step_kernel<256><<<grid, kThreads, 0, s>>>(p); break;
+        case 16: return launch(step_kernel<16>, grid, kThreads, 0, s, first, p);
+        case 32: return launch(step_kernel<32>, grid, kThreads, 0, s, first, p);
+        case 64: return launch(step_kernel<64>, grid, kThreads, 0, s, first, p);
+        case 128: return launch(step_kernel<128>, grid, kThreads, 0, s, first, p);
+        default: return launch(step_kernel<256>, grid, kThreads, 0, s, first, p);
     }
-    return cudaGetLastError();
 }
 
 int launch_out(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s) {

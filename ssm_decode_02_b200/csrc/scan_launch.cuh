@@ -1,0 +1,39 @@
+// scan_launch.cuh -- the kernels of one call, launched so that they follow one another
+// without a gap (programmatic dependent launch).
+//
+// A kernel's blocks start where SMs are free once every block of the one before has
+// called let_next() or ended; wait_before() holds them until that one is complete, with
+// all that it wrote.  Every block calls wait_before() before it leaves and before it uses
+// what a kernel before may have written, and let_next() only behind it, so that a
+// complete kernel always means that those before it are complete as well.  The first
+// kernel of a call starts after all that is in the stream.
+//
+// Kernels of several rounds of blocks do not call let_next(): with the next kernel's
+// blocks placed while the last round ran, the gradient of 4 x 2048 tokens with 80 heads of
+// 128 x 64 took 593 us instead of 562.  A gap costs about 2 us: that gradient 575 us with
+// plain launches, a norm's with its column sums 98.6 against 96.4.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace rsq {
+
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... Formal, class... Actual>
+int launch(void (*kernel)(Formal...), dim3 grid, int threads, size_t smem, cudaStream_t s, bool first, Actual... args) {
+    cudaLaunchAttribute after;
+    after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    after.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &after;
+    c.numAttrs = first ? 0 : 1;
+    return cudaLaunchKernelEx(&c, kernel, static_cast<Formal>(args)...);
+}
+
+}  // namespace rsq

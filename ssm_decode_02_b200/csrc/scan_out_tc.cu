@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kBlock, 1) out_tc_kernel(const __grid_constant
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    wait_before();
     const uint32_t tmem = *tmem_slot;
     const uint32_t lanes = (static_cast<uint32_t>(warp) & 3) << 21;
 
@@ -444,8 +445,8 @@ int run(const Params& p, const tc::Maps& m, int head_set, cudaStream_t s) {
     if (err) return err;
     const long long units = static_cast<long long>(p.slots) * p.G * ((p.per + head_set - 1) / head_set);
     if (units > 2000000000) return cudaErrorInvalidConfiguration;
-    out_tc_kernel<N><<<static_cast<unsigned>(std::min<long long>(units, kSms)), kBlock, Shape<N>::kSmem, s>>>(p, m, head_set, static_cast<int>(units));
-    return cudaGetLastError();
+    return launch(out_tc_kernel<N>, static_cast<unsigned>(std::min<long long>(units, kSms)), kBlock, Shape<N>::kSmem, s, false, p, m, head_set,
+                  static_cast<int>(units));
 }
 
 }  // namespace

@@ -41,12 +41,12 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
                                                                const __grid_constant__ tc::Maps maps) {
     using Sh = Shape<N>;
     extern __shared__ uint8_t raw_smem[];
+    wait_before();
     const Pass& ps = blockIdx.z ? bwd : fwd;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int parts = p.N / N, cb = blockIdx.y / parts, row0 = (blockIdx.y - cb * parts) * N;  // first state row
     const int c0 = cb * kCols, h0 = c0 / p.P, heads = p.P >= kCols ? 1 : 2;
     const int group = h0 / p.per;
-
     int seq, lo, len, slot0, seg_first = 1, seg_last = 1;
     if (p.seg_chunks) {
         const Range r = slot_range(p, blockIdx.x, kChunk * p.seg_chunks);
@@ -282,8 +282,7 @@ int run(const Params& p, const tc::Maps& m, bool backward, const Pass& f, const 
     const int err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<N>::kSmem);
     if (err) return err;
     const dim3 grid(p.seg_chunks ? p.seg_slots : p.n, p.H * p.P / kCols * (p.N / N), backward ? 2 : 1);
-    k<<<grid, kBlock, Shape<N>::kSmem, s>>>(p, f, b, m);
-    return cudaGetLastError();
+    return launch(k, grid, kBlock, Shape<N>::kSmem, s, !p.slots, p, f, b, m);
 }
 
 }  // namespace
