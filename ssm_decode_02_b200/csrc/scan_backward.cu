@@ -9,8 +9,8 @@
 // the gradients of the gates are
 //     dlog a_t = sum_{t'>=t} m_t' + sum_{j<t} dt_j fin_j + 2^b_end <S_0, dS>
 //     ddt_t    = sum_{i>=t} L_it (C_i.B_t)(dout_i.x_t) + fin_t + A dlog a_t
-// (pairs on one side of t cancel in the first sum, which is therefore made from sums
-// by blocks, head_gates in scan.cuh).  They are binary32 outputs: Z comes from products of the inputs alone, and the
+// where sum_{t'>=t} of the Z in m_t' is the sum of Z_ij over i >= t > j, made as such
+// (head_gates, scan.cuh).  They are binary32 outputs: Z comes from products of the inputs alone, and the
 // two state terms from states in three bf16 terms (split3).
 #include "tc.cuh"
 
@@ -58,6 +58,26 @@ __device__ __forceinline__ void zero(float (&a)[N][4]) {
         for (int e = 0; e < 4; ++e) a[i][e] = 0.f;
 }
 
+// A diagonal block of 16 x 16 (rows j, columns i > j; else zero): every column t gets,
+// in the rows before it, the sum of its row from t on.
+__device__ __forceinline__ void around_each(float (&z)[2][4], int g, int q) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float behind = 0.f;             // the columns of the block behind this one
+#pragma unroll
+        for (int nb = 1; nb >= 0; --nb) {
+            float* v = z[nb] + 2 * r;
+            const float t = v[0] + v[1], n1 = __shfl_xor_sync(0xffffffffu, t, 1);
+            const float two = t + n1, n2 = __shfl_xor_sync(0xffffffffu, two, 2);
+            const float rest = ((q & 1) ? 0.f : n1) + (q < 2 ? n2 : 0.f) + behind;
+            const int c = nb * 8 + 2 * q, j = g + 8 * r;
+            v[0] = c > j ? t + rest : 0.f;
+            v[1] = c + 1 > j ? v[1] + rest : 0.f;
+            behind += two + n2;
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // dx and the gates: a block per (chunk, set of heads of one group).
 // ---------------------------------------------------------------------------
@@ -94,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
     const uint32_t sk = smem_u32(smem), sq = sk + Sh::kK, sx = sq + Sh::kK, sy = sx + Sh::kX, sp = sy + Sh::kX;
     float2* b = reinterpret_cast<float2*>(smem + 2 * Sh::kK + 2 * Sh::kX + Sh::kPlanes);
     float* dt = reinterpret_cast<float*>(b + kChunk);
-    float* zrow = dt + kChunk;           // [8][kChunk] sum_{j<i} Z_ij by the warps of j
+    float* zrow = dt + kChunk;           // [8][kChunk] by the warps of j: sum_j Z_ij; in its own block the pairs around i
     float* zcol = zrow + 8 * kChunk;     // [8][kChunk] sum_{i>j} Z_ij / dt_j by the blocks of 16 i
     float* in_i = zcol + 8 * kChunk;     // 2^b_i C_i.(S_0 dout_i)
     float* own = in_i + kChunk;          // Z_jj / dt_j
@@ -217,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
 #pragma unroll
                     for (int nb = 0; nb < 2; ++nb) {
                         const int ci = ib * 16 + nb * 8 + 2 * q;
-                        float pr[4], col[2];
+                        float pr[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int i = ci + (e & 1), j = row0 + g + (e >> 1) * 8;
@@ -234,8 +254,14 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
                         }
                         dir0 += zz[nb][0] + zz[nb][1];
                         dir8 += zz[nb][2] + zz[nb][3];
-                        col[0] = fmaf(dt0, zz[nb][0], dt8 * zz[nb][2]);
-                        col[1] = fmaf(dt0, zz[nb][1], dt8 * zz[nb][3]);
+                        a[2 * nb] = pack(pr[0], pr[1]);
+                        a[2 * nb + 1] = pack(pr[2], pr[3]);
+                    }
+                    if (ib == warp) around_each(zz, g, q);
+#pragma unroll
+                    for (int nb = 0; nb < 2; ++nb) {
+                        const int ci = ib * 16 + nb * 8 + 2 * q;
+                        float col[2] = {fmaf(dt0, zz[nb][0], dt8 * zz[nb][2]), fmaf(dt0, zz[nb][1], dt8 * zz[nb][3])};
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) {
                             col[0] += __shfl_xor_sync(0xffffffffu, col[0], d);
@@ -245,8 +271,6 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
                             zrow[warp * kChunk + ci] += col[0];
                             zrow[warp * kChunk + ci + 1] += col[1];
                         }
-                        a[2 * nb] = pack(pr[0], pr[1]);
-                        a[2 * nb + 1] = pack(pr[2], pr[3]);
                     }
                     dir0 = quad_sum(dir0);
                     dir8 = quad_sum(dir8);
@@ -525,22 +549,23 @@ __global__ void __launch_bounds__(kThreads, 1) dk_kernel(const __grid_constant__
     }
 }
 
-// dA, dD: sums of the chunks' parts, eight interleaved runs in order.
+// dA, dD: sums of the chunks' parts, eight interleaved runs in order, in binary64: thousands
+// of parts whose signs differ.
 __global__ void __launch_bounds__(256) sums_kernel(const __grid_constant__ Params p) {
-    __shared__ float sh[8][33];
+    __shared__ double sh[8][33];
     wait_before();
     const int h = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
     float* out = blockIdx.y ? p.dD : p.dA;
     if (!out) return;
     const float* part = p.part + static_cast<long long>(blockIdx.y) * p.slots * p.H;
-    float s = 0.f;
+    double s = 0.;
     if (h < p.H)
         for (int i = w; i < p.slots; i += 8) s += part[static_cast<long long>(i) * p.H + h];
     sh[w][threadIdx.x & 31] = s;
     __syncthreads();
     if (w == 0 && h < p.H) {
         for (int i = 1; i < 8; ++i) s += sh[i][threadIdx.x];
-        out[h] = s;
+        out[h] = static_cast<float>(s);
     }
 }
 

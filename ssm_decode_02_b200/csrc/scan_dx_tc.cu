@@ -212,6 +212,12 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                     for (int q = 0; q < 8; ++q) o[s * 8 + q] = pack(g[2 * q], g[2 * q + 1]);
                 }
                 tc::tmem_st16(dst, o);
+                if (diagonal) {                                 // the pairs around each column
+#pragma unroll
+                    for (int q = 30; q >= 0; --q) v[q] += v[q + 1];
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) v[q] = q <= lane ? 0.f : v[q];
+                }
                 out[kCol + quarter * 128 + cols * 32 + lane] = transpose_sum(v, lane);
                 out[kRow + cols * 128 + row] = rows;
                 if (diagonal) out[kOwn + row] = own;
