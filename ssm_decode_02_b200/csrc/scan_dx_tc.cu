@@ -166,10 +166,10 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                 fac[lane] = ex2_diff(bk, bm);
                 if (direct) pair[lane] = bk;
                 __syncwarp();
-                float v[32], own = 0.f, rows = 0.f;
+                float v[32], own = 0.f, rows = 0.f, run = 0.f;
                 uint32_t o[16];
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
+                for (int s = 1; s >= 0; --s) {
                     float g[16], w[16];
                     tc::tmem_ld16(g, tmem + kG + cols * 32 + s * 16 + lanes);
                     tc::tmem_ld16(w, tmem + kW + cols * 32 + s * 16 + lanes);
@@ -193,31 +193,27 @@ __global__ void __launch_bounds__(kBlock, 1) dx_tc_kernel(const __grid_constant_
                     }
                     if (diagonal) {
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) {
+                        for (int q = 15; q >= 0; --q) {         // v: the pairs around each column
                             const int c = s * 16 + q;
                             g[q] = c < lane ? 0.f : g[q];
-                            if (c == lane) own = w[q] * g[q];
-                            w[q] = c <= lane ? 0.f : w[q] * g[q];
+                            const float z = w[q] * g[q];
+                            if (c == lane) own = z;
+                            rows += c > lane ? z : 0.f;
+                            run = fmaf(z, dt, run);
+                            v[c] = c > lane ? run : 0.f;
                         }
                     } else {
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) w[q] *= g[q];
-                    }
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) {
-                        rows += w[q];
-                        v[s * 16 + q] = w[q] * dt;
+                        for (int q = 0; q < 16; ++q) {
+                            const float z = w[q] * g[q];
+                            rows += z;
+                            v[s * 16 + q] = z * dt;
+                        }
                     }
 #pragma unroll
                     for (int q = 0; q < 8; ++q) o[s * 8 + q] = pack(g[2 * q], g[2 * q + 1]);
                 }
                 tc::tmem_st16(dst, o);
-                if (diagonal) {                                 // the pairs around each column
-#pragma unroll
-                    for (int q = 30; q >= 0; --q) v[q] += v[q + 1];
-#pragma unroll
-                    for (int q = 0; q < 32; ++q) v[q] = q <= lane ? 0.f : v[q];
-                }
                 out[kCol + quarter * 128 + cols * 32 + lane] = transpose_sum(v, lane);
                 out[kRow + cols * 128 + row] = rows;
                 if (diagonal) out[kOwn + row] = own;
