@@ -12,6 +12,14 @@
 // With n = u r, r = 1/sqrt(mean(u^2) + eps) and dn the gradient of n:
 //     du = r (dn - n mean(dn n)),   mean(dn n) = r mean(dn u)
 // so the two sums of a backward row, u^2 and dn u, share one reduction.
+//
+// Measured: gated norm of 16384 x 5120 bf16 84 us (6.0 TB/s, 91% of the measured copy
+// rate), residual norm of as many bytes 88 us; gradients 96 us (8192 x 5120, 420 MB) and
+// 80 us (8192 x 2560 with a binary32 stream, 378 MB), 66 and 72% -- bound by the chain of a
+// row (load, two passes, reduction), of which 96 registers a thread let an SM hold few.
+// Rows on their way to shared memory by cp.async (107 to 159 us), paired binary32
+// arithmetic (135), one vector a thread (126 to 170) and fewer registers (spills) were
+// slower.  A step's few rows are one launch: 3 us in a graph.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -285,7 +285,7 @@ __device__ __forceinline__ void store_rows(bf16* dst, long long stride, int row0
 // within c.  No sum here is the difference of two others: every pair from t on, less
 // those on t's one side, left up to 40 times the rounding error in dA, a sum over the
 // tokens (over a whole chunk; 2 to 8 times within blocks of 32).  The sums around each
-// token of a block cost 2% of a gradient (572 us against 561, 4 x 2048 tokens, 80 heads
+// token of a block cost 2% of a gradient (586 us against 575, 4 x 2048 tokens, 80 heads
 // of 128 x 64).
 // ---------------------------------------------------------------------------
 struct HeadSums {

@@ -9,7 +9,10 @@
 // M is rounded to bf16 once, after the sum.  M lies in tensor memory, where the
 // scorers add to it; the other two sums lie in registers, a thread one row of 64.
 // Warps, which meet at mbarriers only:
-//   8 scorers, 4 + 4 summers, 4 converters (states to bf16), 2 loaders, 1 issuer.
+//   8 scorers, 4 + 4 summers, 4 converters (states to bf16), 3 loaders, 1 issuer.
+// 128 blocks, one round, on 148 SMs, each bound by the chain through its roles (46% of the
+// issue slots, 13% of the tensor cycles): 4 x 2048 tokens, 80 heads of 128 x 64, 150 us;
+// 520 with warp products.
 #include "tc.cuh"
 
 namespace rsq {

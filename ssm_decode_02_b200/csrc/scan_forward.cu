@@ -11,7 +11,8 @@ namespace {
 // head).  The sum is binary64 and stays as two floats: differences of two such
 // sums, which become the decays between tokens, keep binary32 accuracy behind
 // strong decays and behind a decay of zero.  Rows past the end of the sequence
-// have a_t = 1 and dt = 0.
+// have a_t = 1 and dt = 0.  Bound by latency and by what it writes: 11 us for 16384
+// tokens and 80 heads (21 MB).
 // ---------------------------------------------------------------------------
 constexpr int kGateHeads = kThreads / 32;   // of a block
 
@@ -83,7 +84,9 @@ __global__ void __launch_bounds__(kThreads) gates_kernel(const __grid_constant__
 // product.  The weights 2^(b_end-b_j) dt_j go on the key operand, in three bf16
 // terms (scan.cuh, split3): the state stays accurate to binary32.
 // The backward recurrence is the same with (C, dout, 2^b_i) for (B, x, weights)
-// and the chunks in reverse.
+// and the chunks in reverse.  Bound by the issue of split3 and of the warp products:
+// 292 us for 8 x 2048 tokens, 80 heads of 128 x 64, where scan_states_tc.cu, which has
+// the shapes from dk = 64 on, takes 126 to 133.
 // ---------------------------------------------------------------------------
 template <int N>
 struct StateShape {
@@ -307,7 +310,8 @@ __global__ void __launch_bounds__(kThreads) segments_kernel(const __grid_constan
 // The decay between two tokens of different 16-token blocks is the product of
 // two powers that meet at the end of the earlier block, both at most 1 where
 // decays are: a table of dt_j 2^(b_e - b_j) per head and one power per row and
-// block take the place of one power per pair.
+// block take the place of one power per pair.  Bound by instruction issue: 315 us for 8 x
+// 2048 tokens, 80 heads of 128 x 64 (scan_out_tc.cu, which has dk of 64 and 128: 150).
 // ---------------------------------------------------------------------------
 template <int N>
 struct OutShape {
@@ -486,7 +490,9 @@ __global__ void __launch_bounds__(kThreads, N <= 128 ? 2 : 1) out_kernel(const _
 // with a tile of 64 state columns of one head in registers.  A thread owns four
 // columns of every kLanes-th row; the readout is summed over a warp's lanes of
 // the same columns, then over the warps.  Bound by the states' one read and one
-// write; the next chunk kernels would make a pass over the states more.
+// write: 128 sequences, 80 heads of 128 x 64, one token: 111 us back to back, 6.04 TB/s,
+// 92% of the measured copy rate.  The chunk kernels would make a pass over the states
+// more.
 // ---------------------------------------------------------------------------
 template <int N>
 __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ Params p) {

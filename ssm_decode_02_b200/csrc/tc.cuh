@@ -93,7 +93,7 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool a_mn, bool b_mn) {
 }
 // One lane of a converged warp.  The issuing warps stay together and enter only the
 // products this way: descriptors are then computed once for the warp (uniform
-// registers); one lane on its own took about 100 cycles per product to issue them.
+// registers); with one lane in a branch of its own a gradient took 622 us instead of 588.
 __device__ __forceinline__ bool elect() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
