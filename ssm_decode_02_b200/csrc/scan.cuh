@@ -41,6 +41,7 @@ struct Params {
     int ragged;
     int tokens, len;              // rows of the token arrays; length of a sequence (not ragged)
     int steps;                    // ragged forward: sequences of so many tokens at most are step_kernel's
+    int longs;                    // blocks of the states' kernels for the others of them (0: one for each sequence)
     const int32_t* cu;
     int slots;                    // chunk slots
     int seg_chunks, seg_slots;    // chunks of a segment (0: whole sequences), segment slots
@@ -93,6 +94,23 @@ __device__ __forceinline__ void sequence(const Params& p, int b, int& lo, int& l
     }
     lo = min(max(__ldg(p.cu + b), 0), p.tokens);
     len = min(max(__ldg(p.cu + b + 1), lo), p.tokens) - lo;
+}
+
+// The k-th sequence of more than p.steps tokens, or -1.  By a whole warp.
+__device__ __forceinline__ int long_sequence(const Params& p, int k) {
+    for (int i0 = 0; i0 < p.n; i0 += 32) {
+        const int i = i0 + (threadIdx.x & 31);
+        int lo, len = 0;
+        if (i < p.n) sequence(p, i, lo, len);
+        unsigned m = __ballot_sync(0xffffffffu, len > p.steps);
+        const int c = __popc(m);
+        if (k < c) {
+            for (; k; --k) m &= m - 1;
+            return i0 + __ffs(m) - 1;
+        }
+        k -= c;
+    }
+    return -1;
 }
 
 // First slot of sequence b when slots hold `unit` rows each.  Equal lengths:

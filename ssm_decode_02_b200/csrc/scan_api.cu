@@ -17,6 +17,10 @@ constexpr int64_t kMaxTokens = (1LL << 31) - (1LL << 17);
 // sequences 4.9, 15 and 27 us against 44; 16 of 16 heads of 128 x 128 6.8, 22 and 40
 // against 43.
 constexpr int kStepTokens = 12;
+// Up to so many sequences of a ragged batch the states' blocks look for the long ones
+// (long_sequence), of which there are at most tokens / 13: a block without work costs
+// about 1 us of an SM, a look through 32 sequences a tenth of that.
+constexpr int kLookThrough = 2048;
 
 bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128 || d == 256; }
 bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -245,7 +249,11 @@ rsq_status rsq_scan(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs, c
     p.out = static_cast<bf16*>(out);
     auto s = static_cast<cudaStream_t>(stream);
     if (steps) return done("scan", launch_step(p, s));
-    p.steps = cfg->ragged ? kStepTokens : 0;
+    if (cfg->ragged) {
+        p.steps = kStepTokens;
+        const int most = p.tokens / (kStepTokens + 1);
+        if (p.n <= kLookThrough && most < p.n) p.longs = std::max(1, most);
+    }
     tc::Maps m{};
     int err = maps_for(p, false, &m);
     if (!err) err = p.slots ? launch_gates(p, s) : cudaMemsetAsync(p.flag, 0, sizeof(unsigned), s);

@@ -121,7 +121,8 @@ __global__ void __launch_bounds__(kThreads) states_kernel(const __grid_constant_
         seg_first = r.index == 0;
         seg_last = lo + len == r.seq_first + r.seq_len;
     } else {
-        seq = blockIdx.x;
+        seq = p.longs ? long_sequence(p, blockIdx.x) : static_cast<int>(blockIdx.x);
+        if (seq < 0) return;
         sequence(p, seq, lo, len);
         if (p.steps && len <= p.steps) return;
         slot0 = first_slot(p, seq, lo, kChunk);
@@ -585,7 +586,7 @@ template <int N>
 int states_n(const Params& p, const tc::Maps& m, bool backward, const Pass& f, const Pass& b, cudaStream_t s) {
     using Sh = StateShape<N>;
     if (N >= 64 && states_tc_ok(p)) return launch_states_tc(p, m, backward, f, b, s);
-    const dim3 grid(p.seg_chunks ? p.seg_slots : p.n, p.H * p.tiles, backward ? 2 : 1);
+    const dim3 grid(p.seg_chunks ? p.seg_slots : (p.longs ? p.longs : p.n), p.H * p.tiles, backward ? 2 : 1);
     auto* k = backward ? states_kernel<N, true> : states_kernel<N, false>;
     const int err = allow_smem(k, Sh::kSmem);
     if (err) return err;

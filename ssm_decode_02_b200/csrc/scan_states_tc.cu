@@ -62,7 +62,8 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
         seg_first = r.index == 0;
         seg_last = lo + len == r.seq_first + r.seq_len;
     } else {
-        seq = blockIdx.x;
+        seq = p.longs ? long_sequence(p, blockIdx.x) : static_cast<int>(blockIdx.x);
+        if (seq < 0) return;
         sequence(p, seq, lo, len);
         if (p.steps && len <= p.steps) return;
         slot0 = first_slot(p, seq, lo, kChunk);
@@ -285,7 +286,7 @@ int run(const Params& p, const tc::Maps& m, bool backward, const Pass& f, const 
     auto* k = backward ? states_tc_kernel<N, true> : states_tc_kernel<N, false>;
     const int err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<N>::kSmem);
     if (err) return err;
-    const dim3 grid(p.seg_chunks ? p.seg_slots : p.n, p.H * p.P / kCols * (p.N / N), backward ? 2 : 1);
+    const dim3 grid(p.seg_chunks ? p.seg_slots : (p.longs ? p.longs : p.n), p.H * p.P / kCols * (p.N / N), backward ? 2 : 1);
     return launch(k, grid, kBlock, Shape<N>::kSmem, s, !p.slots, p, f, b, m);
 }
 

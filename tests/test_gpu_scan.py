@@ -112,6 +112,21 @@ def test_forward_ragged(bounds, tokens, H, N, P, G):
     check_forward(d, bounds, *forward(d, bounds, True, n))
 
 
+MOSTLY_SHORT = [[13] * 10 + [0],                                   # as many long ones as the tokens allow
+                [200] + [1] * 70 + [12, 13, 0, 140] + [1] * 30 + [129],
+                [1, 0, 3, 12] * 12 + [300], [12] * 40]
+
+
+@pytest.mark.parametrize("lengths", MOSTLY_SHORT)
+@pytest.mark.parametrize("H,N,P", [(2, 128, 64), (3, 32, 32)])
+def test_forward_mostly_short(lengths, H, N, P):
+    bounds = [0]
+    for k in lengths:
+        bounds.append(bounds[-1] + k)
+    d, bounds = make(len(lengths), bounds[-1], H, N, P, 1, bounds=bounds, seed=len(lengths))
+    check_forward(d, bounds, *forward(d, bounds, True, len(lengths)))
+
+
 @pytest.mark.parametrize("decay", [False, True])
 def test_forward_strong_decays_and_restarts(decay):
     """Decays of zero (a restart) and far below the smallest float, next to slow ones."""
