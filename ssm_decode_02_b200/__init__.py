@@ -609,6 +609,17 @@ def mamba2_inputs(x, Bm, Cm, dt, A, D, decay=None) -> rsq_mamba2_inputs:
     return rsq_mamba2_inputs(_dptr(x), _dptr(Bm), _dptr(Cm), _dptr(dt), _dptr(A), _dptr(D), _dptr(decay))
 
 
+def _row_stride(t, row: int, what: str) -> int:
+    """Stride of a tensor's rows of `row` elements, 0 for one row.  Rows that share memory are
+    refused: those of a broadcast tensor have stride 0, which is "packed" to the kernels."""
+    if t.shape[0] < 2:
+        return 0
+    s = int(t.stride(0))
+    if s < row:
+        raise ValueError("%s: rows of %d elements lie %d apart (a broadcast tensor has to be copied out)" % (what, row, s))
+    return s
+
+
 def _token_rows(t, what: str) -> tuple[int | None, int]:
     """Address and token stride of a [tokens, ...] argument whose token rows are packed
     but may lie apart (a slice of a projection's output)."""
@@ -620,7 +631,7 @@ def _token_rows(t, what: str) -> tuple[int | None, int]:
             raise ValueError("%s: the row of one token has to be contiguous" % what)
         inner *= t.shape[d]
     p = _dptr(t) if t.dim() < 2 or t.is_contiguous() else _dptr(t[:1].view(-1)) if t.shape[0] else _dptr(t[:1])
-    return p, int(t.stride(0)) if t.dim() > 1 and t.shape[0] > 1 else 0
+    return p, _row_stride(t, inner, what) if t.dim() > 1 else 0
 
 
 def scan_inputs(x, Bm, Cm, dt=None, A=None, D=None, decay=None) -> rsq_scan_inputs:
@@ -651,11 +662,9 @@ def norm_config(x, side, y, *, group: int = 0, order: int = RSQ_NORM_GATE, eps: 
     if side is not None and tuple(side.shape) != (rows, width):
         raise ValueError("x has shape %s, the other input %s" % (tuple(x.shape), tuple(side.shape)))
 
-    def stride(t):
-        return int(t.stride(0)) if t is not None and rows > 1 else 0
     return rsq_norm_config(rows, width, int(group), int(order), _dtype_of(x),
-                           RSQ_F32 if side is None else _dtype_of(side), _dtype_of(y), float(eps), stride(x),
-                           stride(side))
+                           RSQ_F32 if side is None else _dtype_of(side), _dtype_of(y), float(eps), _row_stride(x, width, "x"),
+                           0 if side is None else _row_stride(side, width, "z or residual"))
 
 
 class Scan:

@@ -1,0 +1,109 @@
+"""What the Python binding of the scan and the norms refuses before a kernel sees it
+(no GPU: tensors are stand-ins whose address is never followed, and no call goes
+through)."""
+import pytest
+import torch
+
+import ssm_decode_02_b200 as rsq
+
+P = 1 << 20
+BF = torch.bfloat16
+T, H, N, D, G = 256, 4, 64, 64, 1
+
+
+class Fake:
+    """A CUDA tensor of given shape and strides without memory."""
+
+    def __init__(self, t, device=0):
+        self.t, self.at, self.is_cuda = t, device, True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def __getitem__(self, i):
+        return Fake(self.t[i], self.at)
+
+    def view(self, *shape):
+        return Fake(self.t.view(*shape), self.at)
+
+    def expand(self, *shape):
+        return Fake(self.t.expand(*shape), self.at)
+
+    def data_ptr(self):
+        return P
+
+    def get_device(self):
+        return self.at
+
+
+def on(*shape, dtype=torch.float32, device=0):
+    return Fake(torch.empty(shape, dtype=dtype, device="meta"), device)
+
+
+class Calls:
+    """In the place of the library: records the names of the functions called, all of which succeed."""
+
+    def __init__(self):
+        self.names = []
+
+    def __getattr__(self, name):
+        def call(*a):
+            self.names.append(name)
+            return rsq.RSQ_OK
+        return call
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    c = Calls()
+    monkeypatch.setattr(rsq, "_current_device", lambda: 0)
+    monkeypatch.setattr(rsq, "_stream", lambda s: 0)
+    monkeypatch.setattr(rsq, "lib", c)
+    return c
+
+
+def scan_of(**kw):
+    s = rsq.Scan.__new__(rsq.Scan)
+    s.cfg = rsq.rsq_scan_config(**(dict(family=rsq.RSQ_MAMBA2, in_dtype=rsq.RSQ_BF16, sequences=2, heads=H, dk=N, dv=D, ngroups=G,
+                                        ragged=0, tokens=T) | kw))
+    return s
+
+
+def tokens(**kw):
+    return dict(x=on(T, H, D, dtype=BF), Bm=on(T, G, N, dtype=BF), Cm=on(T, G, N, dtype=BF), dt=on(T, H), A=on(H), D=on(H)) | kw
+
+
+def slices(*widths, rows=T):
+    """Column ranges of one wide array."""
+    wide = on(rows, sum(widths) + 8, dtype=BF)
+    at = [sum(widths[:i]) for i in range(len(widths))]
+    return [wide[:, a:a + w] for a, w in zip(at, widths)]
+
+
+# ------------------------------------------------------------------------------- rows of a tensor
+@pytest.mark.parametrize("name,t", [("x", on(1, H, D, dtype=BF).expand(T, H, D)), ("Bm", on(1, G, N, dtype=BF).expand(T, G, N)),
+                                    ("Cm", on(1, G, N, dtype=BF).expand(T, G, N)),
+                                    ("Cm", Fake(torch.empty(T * N, dtype=BF, device="meta").as_strided((T, G, N), (8, N, 1))))])
+def test_scan_refuses_rows_that_share_memory(calls, name, t):
+    """A broadcast tensor has one row stored; a stride of 0 means packed rows to the kernels."""
+    with pytest.raises(ValueError, match=name):
+        rsq.scan_inputs(**tokens(**{name: t}))
+
+
+def test_scan_takes_rows_that_lie_apart(calls):
+    x, Bm, Cm = slices(H * D, N, N)
+    ins = rsq.scan_inputs(**tokens(x=x.view(T, H, D), Bm=Bm.view(T, 1, N), Cm=Cm.view(T, 1, N)))
+    assert ins.x_stride == ins.b_stride == ins.c_stride == H * D + 2 * N + 8
+    scan_of().forward(ins, on(T, H, D, dtype=BF))
+    one = tokens(x=on(1, H, D, dtype=BF).expand(1, H, D), Bm=on(1, G, N, dtype=BF), Cm=on(1, G, N, dtype=BF), dt=on(1, H))
+    scan_of(sequences=1, tokens=1).forward(rsq.scan_inputs(**one), on(1, H, D, dtype=BF))
+    assert calls.names == ["rsq_scan", "rsq_scan"]
+
+
+def test_norm_config_refuses_rows_that_share_memory(calls):
+    x = on(T, N, dtype=BF)
+    for a, b in [(on(1, N, dtype=BF).expand(T, N), x), (x, on(1, N, dtype=BF).expand(T, N)), (on(N, dtype=BF).expand(T, N), None),
+                 (x, Fake(torch.empty(4 * T + N, dtype=BF, device="meta").as_strided((T, N), (4, 1))))]:
+        with pytest.raises(ValueError, match="row"):
+            rsq.norm_config(a, b, BF)
+    assert rsq.norm_config(on(N, dtype=BF).expand(1, N), None, BF).x_stride == 0
