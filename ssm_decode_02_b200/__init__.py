@@ -533,15 +533,43 @@ def _norm_sized(cfg, x, side, y, w) -> None:
         pass
 
 
+def _rows_as(t, rows: int, width: int, stride: int, what: str) -> None:
+    """Refuses a tensor whose rows lie other than `stride` (0: packed) says: the kernels go by the
+    configuration, whichever tensors it was made from."""
+    if t is None or isinstance(t, int) or rows < 2:
+        return
+    stride = stride or width
+    dim = t.dim()
+    if dim > 1 and t.stride(0) == stride and t.shape[0] >= rows:
+        if dim == 2 and t.shape[1] >= width:
+            return
+        inner = 1
+        for d in range(dim - 1, 0, -1):
+            if t.shape[d] > 1 and t.stride(d) != inner:
+                break
+            inner *= t.shape[d]
+        else:
+            if inner >= width:
+                return
+    if stride == width and t.is_contiguous():
+        return
+    raise ValueError("%s: the configuration has %d rows of %d columns, %d elements apart; got shape %s with strides %s"
+                     % (what, rows, width, stride, tuple(t.shape), tuple(t.stride())))
+
+
 def rsq_gated_norm(cfg: rsq_norm_config, x, z, w, y, stream=None) -> None:
-    """x and z may be row-strided (norm_config reads their strides)."""
+    """x and z may be row-strided, as the configuration says (norm_config reads their strides)."""
     _norm_sized(cfg, x, z, y, w)
+    _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
+    _rows_as(z, cfg.rows, cfg.width, cfg.side_stride, "z")
     _check(lib.rsq_gated_norm(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(z), _dptr(w), _dptr(y),
                               _stream(stream)))
 
 
 def rsq_gated_norm_backward(cfg: rsq_norm_config, x, z, w, dy, dx, dz, dw, workspace=None, stream=None) -> None:
     _norm_sized(cfg, x, z, dy, w)
+    _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
+    _rows_as(z, cfg.rows, cfg.width, cfg.side_stride, "z")
     _sized(cfg.rows * cfg.width, _ITEM.get(cfg.x_dtype, 0), dx=dx)
     _sized(cfg.rows * cfg.width, _ITEM.get(cfg.side_dtype, 0), dz=dz)
     _sized(cfg.width, 4, dw=dw)
@@ -551,8 +579,10 @@ def rsq_gated_norm_backward(cfg: rsq_norm_config, x, z, w, dy, dx, dz, dw, works
 
 
 def rsq_residual_norm(cfg: rsq_norm_config, x, residual, scale, w, h, y, stream=None) -> None:
-    """x and residual may be row-strided (norm_config reads their strides)."""
+    """x and residual may be row-strided, as the configuration says (norm_config reads their strides)."""
     _norm_sized(cfg, x, residual, y, w)
+    _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
+    _rows_as(residual, cfg.rows, cfg.width, cfg.side_stride, "residual")
     if h is not residual:
         _sized(cfg.rows * cfg.width, _ITEM.get(cfg.side_dtype, 0), h=h)
     if scale is not None:
@@ -564,6 +594,7 @@ def rsq_residual_norm(cfg: rsq_norm_config, x, residual, scale, w, h, y, stream=
 def rsq_residual_norm_backward(cfg: rsq_norm_config, x, h, scale, w, dy, dh, dx, dresidual, dscale, dw,
                                workspace=None, stream=None) -> None:
     _norm_sized(cfg, x, h, dy, w)
+    _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
     _sized(cfg.rows * cfg.width, _ITEM.get(cfg.side_dtype, 0), dh=dh, dresidual=dresidual)
     _sized(cfg.rows * cfg.width, _ITEM.get(cfg.x_dtype, 0), dx=dx)
     _sized(cfg.width, 4, scale=scale, dw=dw, dscale=dscale)

@@ -107,3 +107,50 @@ def test_norm_config_refuses_rows_that_share_memory(calls):
         with pytest.raises(ValueError, match="row"):
             rsq.norm_config(a, b, BF)
     assert rsq.norm_config(on(N, dtype=BF).expand(1, N), None, BF).x_stride == 0
+
+
+def norm_cfg(rows=T, width=N, x_stride=0, side_stride=0, x=rsq.RSQ_BF16, side=rsq.RSQ_BF16, y=rsq.RSQ_BF16):
+    return rsq.rsq_norm_config(rows, width, 0, 0, x, side, y, 1e-5, x_stride, side_stride)
+
+
+def norm_calls(cfg, x, side):
+    """Every norm call that reads x and side (z, or the residual) by the configuration's strides."""
+    w, y = on(N), on(T, N, dtype=BF)
+    h = y if side is None else on(T, N, dtype=side.dtype)
+    return [lambda: rsq.rsq_gated_norm(cfg, x, side, w, y), lambda: rsq.rsq_gated_norm_backward(cfg, x, side, w, y, None, None, None),
+            lambda: rsq.rsq_residual_norm(cfg, x, side, None, w, h, y)]
+
+
+def test_norms_refuse_rows_that_lie_other_than_configured(calls):
+    """A configuration is made once and used with other tensors: a packed tensor read at a slice's
+    stride is left behind its end."""
+    packed, (a, b) = on(T, N, dtype=BF), slices(N, N)
+    apart = int(a.stride(0))
+    wrong = [(norm_cfg(x_stride=apart), packed, packed), (norm_cfg(side_stride=apart), packed, packed), (norm_cfg(), a, packed),
+             (norm_cfg(), packed, b), (norm_cfg(x_stride=apart, side_stride=apart), a, packed),
+             (norm_cfg(x_stride=apart), on(T - 1, apart, dtype=BF)[:, :N], packed),
+             (norm_cfg(x_stride=apart), on(T, apart, dtype=BF)[:, :N - 8], None),
+             (norm_cfg(), on(1, N, dtype=BF).expand(T, N), packed), (norm_cfg(), packed, on(1, N, dtype=BF).expand(T, N)),
+             (norm_cfg(x_stride=apart), on(T, 2, apart // 2, dtype=BF)[:, :, :N // 2], None)]
+    for cfg, x, side in wrong:
+        for call in norm_calls(cfg, x, side):
+            with pytest.raises(ValueError):
+                call()
+    cfg = norm_cfg(x_stride=apart, side=rsq.RSQ_F32)
+    with pytest.raises(ValueError):
+        rsq.rsq_residual_norm_backward(cfg, packed, on(T, N), None, on(N), packed, None, None, None, None, None)
+    assert not calls.names
+
+
+def test_norms_take_rows_as_configured(calls):
+    packed, (a, b) = on(T, N, dtype=BF), slices(N, N)
+    apart = int(a.stride(0))
+    right = [(norm_cfg(), packed, packed), (norm_cfg(x_stride=N, side_stride=N), packed, packed), (norm_cfg(x_stride=apart), a, packed),
+             (norm_cfg(x_stride=apart, side_stride=apart), a, b), (norm_cfg(), packed.view(T * N), packed.view(T // 2, 2 * N)),
+             (norm_cfg(rows=1), a[:1], b[:1]), (norm_cfg(x_stride=apart), a.view(T, 2, N // 2), None), (norm_cfg(rows=T - 3), packed, packed)]
+    for cfg, x, side in right:
+        for call in norm_calls(cfg, x, side):
+            call()
+    # the backward pass has h as the forward pass wrote it, whatever the residual's stride was
+    rsq.rsq_residual_norm_backward(norm_cfg(side_stride=apart), packed, packed, None, on(N), packed, None, None, None, None, None)
+    assert len(calls.names) == 3 * len(right) + 1
