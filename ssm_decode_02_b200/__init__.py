@@ -232,12 +232,26 @@ def _current_device() -> int:
     return _current_device()
 
 
-def _sized(count: int, item: int, **tensors) -> None:
-    """Refuses tensors of fewer than count elements, or of elements of other than item bytes:
-    the kernels take their sizes from the configuration alone."""
+_torch_types = None
+
+
+def _types() -> dict:
+    """torch dtypes by rsq_dtype; int32 by its name."""
+    global _torch_types
+    if _torch_types is None:
+        import torch
+        _torch_types = {RSQ_F32: torch.float32, RSQ_BF16: torch.bfloat16, "int32": torch.int32}
+    return _torch_types
+
+
+def _sized(count: int, type_, **tensors) -> None:
+    """Refuses tensors of fewer than count elements, or of another type than type_ (a key of
+    _types; others are the library's to refuse): the kernels take sizes and types from the
+    configuration alone, and read float16 bits as bfloat16."""
+    want = _types().get(type_)
     for name, t in tensors.items():
-        if t is not None and not isinstance(t, int) and (t.numel() < count or t.element_size() != item):
-            raise ValueError("%s: expected at least %d elements of %d bytes, got %s of %s" % (name, count, item, tuple(t.shape), t.dtype))
+        if t is not None and not isinstance(t, int) and (t.numel() < count or (t.dtype is not want and want is not None)):
+            raise ValueError("%s: expected at least %d elements of %s, got %s of %s" % (name, count, want, tuple(t.shape), t.dtype))
 
 
 def _here(t) -> None:
@@ -514,18 +528,16 @@ def rsq_norm_workspace(cfg: rsq_norm_config) -> int:
     return int(n.value)
 
 
-_ITEM = {RSQ_F32: 4, RSQ_BF16: 2}
-
-
 def _norm_sized(cfg, x, side, y, w) -> None:
     """As _sized and _here for what every norm call has, written out: a decode step's call
     takes a few microseconds in all."""
-    n = cfg.rows * cfg.width
+    n, types = cfg.rows * cfg.width, _types()
+    tx, ts, ty = types.get(cfg.x_dtype), types.get(cfg.side_dtype), types.get(cfg.y_dtype)   # None: the library's to refuse
     try:
         if (y.numel() < n or w.numel() < cfg.width
-                or (x is not None and (x.numel() < n or x.element_size() != _ITEM[cfg.x_dtype]))
-                or y.element_size() != _ITEM[cfg.y_dtype] or w.element_size() != 4
-                or (side is not None and (side.numel() < n or side.element_size() != _ITEM[cfg.side_dtype]))):
+                or (x is not None and (x.numel() < n or (x.dtype is not tx and tx)))
+                or (y.dtype is not ty and ty) or w.dtype is not types[RSQ_F32]
+                or (side is not None and (side.numel() < n or (side.dtype is not ts and ts)))):
             raise ValueError("expected %d rows of %d columns in the configuration's types, got %s"
                              % (cfg.rows, cfg.width, [(tuple(t.shape), t.dtype) for t in (x, side, y, w) if t is not None]))
         _here(y)
@@ -570,9 +582,9 @@ def rsq_gated_norm_backward(cfg: rsq_norm_config, x, z, w, dy, dx, dz, dw, works
     _norm_sized(cfg, x, z, dy, w)
     _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
     _rows_as(z, cfg.rows, cfg.width, cfg.side_stride, "z")
-    _sized(cfg.rows * cfg.width, _ITEM.get(cfg.x_dtype, 0), dx=dx)
-    _sized(cfg.rows * cfg.width, _ITEM.get(cfg.side_dtype, 0), dz=dz)
-    _sized(cfg.width, 4, dw=dw)
+    _sized(cfg.rows * cfg.width, cfg.x_dtype, dx=dx)
+    _sized(cfg.rows * cfg.width, cfg.side_dtype, dz=dz)
+    _sized(cfg.width, RSQ_F32, dw=dw)
     ws, n = _workspace(workspace)
     _check(lib.rsq_gated_norm_backward(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(z), _dptr(w), _dptr(dy),
                                        _dptr(dx), _dptr(dz), _dptr(dw), ws, n, _stream(stream)))
@@ -584,9 +596,9 @@ def rsq_residual_norm(cfg: rsq_norm_config, x, residual, scale, w, h, y, stream=
     _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
     _rows_as(residual, cfg.rows, cfg.width, cfg.side_stride, "residual")
     if h is not residual:
-        _sized(cfg.rows * cfg.width, _ITEM.get(cfg.side_dtype, 0), h=h)
+        _sized(cfg.rows * cfg.width, cfg.side_dtype, h=h)
     if scale is not None:
-        _sized(cfg.width, 4, scale=scale)
+        _sized(cfg.width, RSQ_F32, scale=scale)
     _check(lib.rsq_residual_norm(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(residual), _dptr(scale), _dptr(w),
                                  _dptr(h), _dptr(y), _stream(stream)))
 
@@ -595,9 +607,9 @@ def rsq_residual_norm_backward(cfg: rsq_norm_config, x, h, scale, w, dy, dh, dx,
                                workspace=None, stream=None) -> None:
     _norm_sized(cfg, x, h, dy, w)
     _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
-    _sized(cfg.rows * cfg.width, _ITEM.get(cfg.side_dtype, 0), dh=dh, dresidual=dresidual)
-    _sized(cfg.rows * cfg.width, _ITEM.get(cfg.x_dtype, 0), dx=dx)
-    _sized(cfg.width, 4, scale=scale, dw=dw, dscale=dscale)
+    _sized(cfg.rows * cfg.width, cfg.side_dtype, dh=dh, dresidual=dresidual)
+    _sized(cfg.rows * cfg.width, cfg.x_dtype, dx=dx)
+    _sized(cfg.width, RSQ_F32, scale=scale, dw=dw, dscale=dscale)
     ws, n = _workspace(workspace)
     _check(lib.rsq_residual_norm_backward(ctypes.byref(cfg), _dptr_rows(x), _dptr(h), _dptr(scale), _dptr(w),
                                           _dptr(dy), _dptr(dh), _dptr(dx), _dptr(dresidual), _dptr(dscale),
@@ -669,9 +681,8 @@ def scan_inputs(x, Bm, Cm, dt=None, A=None, D=None, decay=None) -> rsq_scan_inpu
     """x [tokens, heads, dv], Bm, Cm [tokens, ngroups, dk]: their tokens may lie apart.  The
     result keeps the tensors that it points at."""
     (xp, xs), (bp, bs), (cp, cs) = _token_rows(x, "x"), _token_rows(Bm, "Bm"), _token_rows(Cm, "Cm")
-    for name, t, item in (("x", x, 2), ("Bm", Bm, 2), ("Cm", Cm, 2), ("dt", dt, 4), ("A", A, 4), ("D", D, 4), ("decay", decay, 4)):
-        if t is not None and not isinstance(t, int) and t.element_size() != item:
-            raise ValueError("%s: expected %s, got %s" % (name, "bfloat16" if item == 2 else "float32", t.dtype))
+    _sized(0, RSQ_BF16, x=x, Bm=Bm, Cm=Cm)
+    _sized(0, RSQ_F32, dt=dt, A=A, D=D, decay=decay)
     ins = rsq_scan_inputs(xp, bp, cp, _dptr(dt), _dptr(A), _dptr(D), _dptr(decay), xs, bs, cs)
     ins.tensors = (x, Bm, Cm, dt, A, D, decay)
     return ins
@@ -723,13 +734,13 @@ class Scan:
         for name, t, row in (("x", x, c.heads * c.dv), ("Bm", Bm, c.ngroups * c.dk), ("Cm", Cm, c.ngroups * c.dk)):
             if t is not None and not isinstance(t, int) and t.numel() != t.shape[0] * row:
                 raise ValueError("%s: expected %d elements a token, got %s" % (name, row, tuple(t.shape)))
-        _sized(c.tokens * c.heads * c.dv, 2, x=x, dx=dx, **{"out": t for t in tokens})
-        _sized(c.tokens * c.ngroups * c.dk, 2, Bm=Bm, Cm=Cm, dBm=dBm, dCm=dCm)
-        _sized(c.tokens * c.heads, 4, dt=dt, decay=decay, ddt=ddt, dlog_decay=dlog)
-        _sized(c.heads, 4, A=A, D=D, dA=dA, dD=dD)
+        _sized(c.tokens * c.heads * c.dv, RSQ_BF16, x=x, dx=dx, **{"out": t for t in tokens})
+        _sized(c.tokens * c.ngroups * c.dk, RSQ_BF16, Bm=Bm, Cm=Cm, dBm=dBm, dCm=dCm)
+        _sized(c.tokens * c.heads, RSQ_F32, dt=dt, decay=decay, ddt=ddt, dlog_decay=dlog)
+        _sized(c.heads, RSQ_F32, A=A, D=D, dA=dA, dD=dD)
         for t in states + (dstate,):
-            _sized(c.sequences * c.heads * c.dk * c.dv, 4, state=t)
-        _sized(c.sequences + 1, 4, cu_seqlens=cu_seqlens)
+            _sized(c.sequences * c.heads * c.dk * c.dv, RSQ_F32, state=t)
+        _sized(c.sequences + 1, "int32", cu_seqlens=cu_seqlens)
 
     def forward(self, inputs, out, *, state_in=None, state_out=None, cu_seqlens=None, workspace=None, stream=None):
         self._fits(inputs, cu_seqlens, states=(state_in, state_out), tokens=(out,))

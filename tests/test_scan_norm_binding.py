@@ -154,3 +154,65 @@ def test_norms_take_rows_as_configured(calls):
     # the backward pass has h as the forward pass wrote it, whatever the residual's stride was
     rsq.rsq_residual_norm_backward(norm_cfg(side_stride=apart), packed, packed, None, on(N), packed, None, None, None, None, None)
     assert len(calls.names) == 3 * len(right) + 1
+
+
+# ------------------------------------------------------------------------------------------ types
+HALF, INT = torch.float16, torch.int32
+
+
+def test_scan_refuses_types_of_the_same_size(calls):
+    """float16 bits are no bfloat16, int32 bits no float32."""
+    for name, t in [("x", on(T, H, D, dtype=HALF)), ("Bm", on(T, G, N, dtype=HALF)), ("Cm", on(T, G, N, dtype=torch.int16)),
+                    ("dt", on(T, H, dtype=INT)), ("A", on(H, dtype=INT)), ("D", on(H, dtype=INT)), ("decay", on(T, H, dtype=INT))]:
+        with pytest.raises(ValueError, match=name):
+            rsq.scan_inputs(**tokens(**{name: t}))
+    ins, out, state, s = rsq.scan_inputs(**tokens()), on(T, H, D, dtype=BF), on(2, H, N, D), scan_of()
+    for kw in [dict(out=on(T, H, D, dtype=HALF)), dict(state_in=on(2, H, N, D, dtype=INT)), dict(state_out=on(2, H, N, D, dtype=INT)),
+               dict(cu_seqlens=on(3)), dict(cu_seqlens=on(3, dtype=torch.uint32))]:
+        with pytest.raises(ValueError):
+            s.forward(ins, **(dict(out=out) | kw))
+    rows = dict(dx=(T, H, D), dBm=(T, G, N), dCm=(T, G, N))
+    single = dict(ddt=(T, H), dlog_decay=(T, H), dA=(H,), dD=(H,), dstate_in=(2, H, N, D))
+    for name, shape in (rows | single).items():
+        with pytest.raises(ValueError):
+            s.backward(ins, out, rsq.scan_grads(**{name: on(*shape, dtype=HALF if name in rows else INT)}))
+    with pytest.raises(ValueError):
+        s.backward(ins, on(T, H, D, dtype=HALF), rsq.scan_grads())
+    with pytest.raises(ValueError):
+        s.backward(ins, out, rsq.scan_grads(), dstate_out=on(2, H, N, D, dtype=INT))
+    assert not calls.names
+    s.forward(ins, out, state_in=state, state_out=state)
+    s.backward(ins, out, rsq.scan_grads(**{k: on(*v, dtype=BF) for k, v in rows.items()}, **{k: on(*v) for k, v in single.items()}),
+               state_in=state, dstate_out=state)
+    scan_of(ragged=1).forward(ins, out, cu_seqlens=on(3, dtype=INT))
+    assert calls.names == ["rsq_scan", "rsq_scan_backward", "rsq_scan"]
+
+
+def test_norms_refuse_types_of_the_same_size(calls):
+    cfg, x, w, half = norm_cfg(), on(T, N, dtype=BF), on(N), on(T, N, dtype=HALF)
+    wide = norm_cfg(x=rsq.RSQ_F32, side=rsq.RSQ_F32, y=rsq.RSQ_F32)
+    f, i, wi = on(T, N), on(T, N, dtype=INT), on(N, dtype=INT)
+    for c, good, bad in ((cfg, x, half), (wide, f, i)):
+        for a in [(bad, good, w, good), (good, bad, w, good), (good, good, w, bad), (good, good, wi, good), (good, None, w, bad)]:
+            with pytest.raises(ValueError):
+                rsq.rsq_gated_norm(c, *a)
+        for k in range(7):
+            a = [good, good, w, good, good, good, w]          # x, z, w, dy, dx, dz, dw
+            a[k] = wi if k in (2, 6) else bad
+            with pytest.raises(ValueError):
+                rsq.rsq_gated_norm_backward(c, *a)
+        for k in range(6):
+            a = [good, good, w, w, good, good]                # x, residual, scale, w, h, y
+            a[k] = wi if k in (2, 3) else bad
+            with pytest.raises(ValueError):
+                rsq.rsq_residual_norm(c, *a)
+        for k in range(10):
+            a = [good, good, w, w, good, good, good, good, w, w]   # x, h, scale, w, dy, dh, dx, dresidual, dscale, dw
+            a[k] = wi if k in (2, 3, 8, 9) else bad
+            with pytest.raises(ValueError):
+                rsq.rsq_residual_norm_backward(c, *a)
+    assert not calls.names
+    bad = norm_cfg()
+    bad.x_dtype = 7                                           # the library's to refuse
+    rsq.rsq_gated_norm(bad, x, x, w, x)
+    assert calls.names == ["rsq_gated_norm"]
