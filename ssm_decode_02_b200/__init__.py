@@ -221,7 +221,9 @@ def _dptr_rows(t) -> int | None:
 def _workspace(t) -> tuple[int | None, int]:
     if t is None:
         return None, 0
-    return _dptr(t), t.numel() * t.element_size()
+    p = _dptr(t)
+    _here(t)
+    return p, t.numel() * t.element_size()
 
 
 def _current_device() -> int:
@@ -247,17 +249,18 @@ def _types() -> dict:
 def _sized(count: int, type_, **tensors) -> None:
     """Refuses tensors of fewer than count elements, or of another type than type_ (a key of
     _types; others are the library's to refuse): the kernels take sizes and types from the
-    configuration alone, and read float16 bits as bfloat16."""
+    configuration alone, and read float16 bits as bfloat16.  Addresses pass."""
     want = _types().get(type_)
     for name, t in tensors.items():
-        if t is not None and not isinstance(t, int) and (t.numel() < count or (t.dtype is not want and want is not None)):
+        if t is not None and hasattr(t, "numel") and (t.numel() < count or (t.dtype is not want and want is not None)):
             raise ValueError("%s: expected at least %d elements of %s, got %s of %s" % (name, count, want, tuple(t.shape), t.dtype))
 
 
-def _here(t) -> None:
-    """Refuses a tensor of another GPU than the current one, whose stream the call uses."""
-    if t is not None and not isinstance(t, int) and t.is_cuda and t.get_device() != _current_device():
-        raise ValueError("the tensors are on cuda:%d, the current device is cuda:%d" % (t.get_device(), _current_device()))
+def _here(*tensors) -> None:
+    """Refuses tensors of another GPU than the current one, whose stream the call uses."""
+    for t in tensors:
+        if t is not None and getattr(t, "is_cuda", False) and t.get_device() != _current_device():
+            raise ValueError("a tensor is on cuda:%d, the current device is cuda:%d" % (t.get_device(), _current_device()))
 
 
 def _dtype_of(t) -> int:
@@ -529,20 +532,17 @@ def rsq_norm_workspace(cfg: rsq_norm_config) -> int:
 
 
 def _norm_sized(cfg, x, side, y, w) -> None:
-    """As _sized and _here for what every norm call has, written out: a decode step's call
+    """As _sized and _here for what every norm call has, without keywords: a decode step's call
     takes a few microseconds in all."""
     n, types = cfg.rows * cfg.width, _types()
-    tx, ts, ty = types.get(cfg.x_dtype), types.get(cfg.side_dtype), types.get(cfg.y_dtype)   # None: the library's to refuse
-    try:
-        if (y.numel() < n or w.numel() < cfg.width
-                or (x is not None and (x.numel() < n or (x.dtype is not tx and tx)))
-                or (y.dtype is not ty and ty) or w.dtype is not types[RSQ_F32]
-                or (side is not None and (side.numel() < n or (side.dtype is not ts and ts)))):
-            raise ValueError("expected %d rows of %d columns in the configuration's types, got %s"
-                             % (cfg.rows, cfg.width, [(tuple(t.shape), t.dtype) for t in (x, side, y, w) if t is not None]))
-        _here(y)
-    except AttributeError:      # addresses
-        pass
+    for t, count, type_ in ((x, n, cfg.x_dtype), (side, n, cfg.side_dtype), (y, n, cfg.y_dtype), (w, cfg.width, RSQ_F32)):
+        if t is None or not hasattr(t, "numel"):
+            continue
+        want = types.get(type_)        # None: the library's to refuse
+        if t.numel() < count or (t.dtype is not want and want is not None):
+            raise ValueError("expected %d rows of %d columns in the configuration's types, got %s of %s"
+                             % (cfg.rows, cfg.width, tuple(t.shape), t.dtype))
+    _here(x, side, y, w)
 
 
 def _rows_as(t, rows: int, width: int, stride: int, what: str) -> None:
@@ -585,6 +585,7 @@ def rsq_gated_norm_backward(cfg: rsq_norm_config, x, z, w, dy, dx, dz, dw, works
     _sized(cfg.rows * cfg.width, cfg.x_dtype, dx=dx)
     _sized(cfg.rows * cfg.width, cfg.side_dtype, dz=dz)
     _sized(cfg.width, RSQ_F32, dw=dw)
+    _here(dx, dz, dw)
     ws, n = _workspace(workspace)
     _check(lib.rsq_gated_norm_backward(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(z), _dptr(w), _dptr(dy),
                                        _dptr(dx), _dptr(dz), _dptr(dw), ws, n, _stream(stream)))
@@ -599,6 +600,7 @@ def rsq_residual_norm(cfg: rsq_norm_config, x, residual, scale, w, h, y, stream=
         _sized(cfg.rows * cfg.width, cfg.side_dtype, h=h)
     if scale is not None:
         _sized(cfg.width, RSQ_F32, scale=scale)
+    _here(h, scale)
     _check(lib.rsq_residual_norm(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(residual), _dptr(scale), _dptr(w),
                                  _dptr(h), _dptr(y), _stream(stream)))
 
@@ -610,6 +612,7 @@ def rsq_residual_norm_backward(cfg: rsq_norm_config, x, h, scale, w, dy, dh, dx,
     _sized(cfg.rows * cfg.width, cfg.side_dtype, dh=dh, dresidual=dresidual)
     _sized(cfg.rows * cfg.width, cfg.x_dtype, dx=dx)
     _sized(cfg.width, RSQ_F32, scale=scale, dw=dw, dscale=dscale)
+    _here(dh, dx, dresidual, scale, dw, dscale)
     ws, n = _workspace(workspace)
     _check(lib.rsq_residual_norm_backward(ctypes.byref(cfg), _dptr_rows(x), _dptr(h), _dptr(scale), _dptr(w),
                                           _dptr(dy), _dptr(dh), _dptr(dx), _dptr(dresidual), _dptr(dscale),
@@ -726,13 +729,14 @@ class Scan:
         return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
     def _fits(self, inputs, cu_seqlens, grads=(None,) * 8, states=(), tokens=()):
-        """Sizes of the tensors behind a call's arguments (the kernels know the configuration's)."""
+        """Sizes, types and devices of the tensors behind a call's arguments (the kernels know the
+        configuration's)."""
         c = self.cfg
         x, Bm, Cm, dt, A, D, decay = getattr(inputs, "tensors", (None,) * 7)
         dx, dBm, dCm, ddt, dlog, dA, dD, dstate = grads
-        _here(x)
+        _here(x, Bm, Cm, dt, A, D, decay, cu_seqlens, *grads, *states, *tokens)
         for name, t, row in (("x", x, c.heads * c.dv), ("Bm", Bm, c.ngroups * c.dk), ("Cm", Cm, c.ngroups * c.dk)):
-            if t is not None and not isinstance(t, int) and t.numel() != t.shape[0] * row:
+            if t is not None and hasattr(t, "numel") and t.numel() != t.shape[0] * row:
                 raise ValueError("%s: expected %d elements a token, got %s" % (name, row, tuple(t.shape)))
         _sized(c.tokens * c.heads * c.dv, RSQ_BF16, x=x, dx=dx, **{"out": t for t in tokens})
         _sized(c.tokens * c.ngroups * c.dk, RSQ_BF16, Bm=Bm, Cm=Cm, dBm=dBm, dCm=dCm)

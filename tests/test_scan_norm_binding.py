@@ -216,3 +216,79 @@ def test_norms_refuse_types_of_the_same_size(calls):
     bad.x_dtype = 7                                           # the library's to refuse
     rsq.rsq_gated_norm(bad, x, x, w, x)
     assert calls.names == ["rsq_gated_norm"]
+
+
+# ---------------------------------------------------------------------------- devices and addresses
+def elsewhere(t):
+    return Fake(t.t, 1)
+
+
+def test_scan_refuses_any_tensor_of_another_device(calls):
+    s, out, state, cu = scan_of(ragged=1), on(T, H, D, dtype=BF), on(2, H, N, D), on(3, dtype=torch.int32)
+    for name in ("x", "Bm", "Cm", "dt", "A", "D", "decay"):
+        a = tokens(decay=on(T, H))
+        with pytest.raises(ValueError, match="cuda:1"):
+            s.forward(rsq.scan_inputs(**(a | {name: elsewhere(a[name])})), out, cu_seqlens=cu)
+    ins = rsq.scan_inputs(**tokens())
+    ws = on(8, dtype=torch.uint8)
+    good = dict(out=out, state_in=state, state_out=state, cu_seqlens=cu, workspace=ws)
+    for name in good:
+        with pytest.raises(ValueError, match="cuda:1"):
+            s.forward(ins, **(good | {name: elsewhere(good[name])}))
+    grads = dict(dx=out, dBm=on(T, G, N, dtype=BF), dCm=on(T, G, N, dtype=BF), ddt=on(T, H), dlog_decay=on(T, H), dA=on(H), dD=on(H),
+                 dstate_in=state)
+    good = dict(dout=out, grads=rsq.scan_grads(**grads), state_in=state, dstate_out=state, cu_seqlens=cu, workspace=ws)
+    for name in good:
+        if name != "grads":
+            with pytest.raises(ValueError, match="cuda:1"):
+                s.backward(ins, **(good | {name: elsewhere(good[name])}))
+    for name in grads:
+        with pytest.raises(ValueError, match="cuda:1"):
+            s.backward(ins, **(good | {"grads": rsq.scan_grads(**(grads | {name: elsewhere(grads[name])}))}))
+    assert not calls.names
+    s.forward(ins, out, state_in=state, state_out=state, cu_seqlens=cu, workspace=ws)
+    s.backward(ins, **good)
+    assert calls.names == ["rsq_scan", "rsq_scan_backward"]
+
+
+def norm_arguments():
+    """Each norm call with the tensors of an ordinary one, by name, in order."""
+    r, w, ws = on(T, N, dtype=BF), on(N), on(8, dtype=torch.uint8)
+    return [(rsq.rsq_gated_norm, dict(x=r, z=r, w=w, y=r)),
+            (rsq.rsq_gated_norm_backward, dict(x=r, z=r, w=w, dy=r, dx=r, dz=r, dw=w, workspace=ws)),
+            (rsq.rsq_residual_norm, dict(x=r, residual=r, scale=w, w=w, h=r, y=r)),
+            (rsq.rsq_residual_norm_backward, dict(x=r, h=r, scale=w, w=w, dy=r, dh=r, dx=r, dresidual=r, dscale=w, dw=w, workspace=ws))]
+
+
+def test_norms_refuse_any_tensor_of_another_device(calls):
+    cfg = norm_cfg()
+    for call, a in norm_arguments():
+        for name in a:
+            with pytest.raises(ValueError, match="cuda:1"):
+                call(cfg, **(a | {name: elsewhere(a[name])}))
+    assert not calls.names
+
+
+def test_an_address_among_tensors_lifts_no_other_check(calls):
+    """An argument may be an address; the others are tensors all the same."""
+    cfg = norm_cfg()
+    for call, a in norm_arguments():
+        for name in a:
+            call(cfg, **(a | ({name: P} if name != "workspace" else {})))
+            for other, t in a.items():
+                if other in (name, "workspace"):
+                    continue
+                few = on(*[d - 1 for d in t.shape], dtype=t.dtype)
+                for bad in (few, on(*t.shape, dtype=torch.float16), elsewhere(t)):
+                    with pytest.raises(ValueError):
+                        call(cfg, **(a | {name: P if name != "workspace" else None, other: bad}))
+    assert len(calls.names) == sum(len(a) for _, a in norm_arguments())
+
+
+def test_host_tensors_and_what_is_no_tensor_are_refused(calls):
+    cfg = norm_cfg()
+    for call, a in norm_arguments():
+        for name, t in a.items():
+            with pytest.raises(ValueError):
+                call(cfg, **(a | {name: torch.empty(t.shape, dtype=t.dtype)}))
+    assert not calls.names
