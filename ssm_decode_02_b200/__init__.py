@@ -503,8 +503,27 @@ def rsq_scan_workspace(cfg: rsq_scan_config, backward: bool = False) -> int:
     return int(n.value)
 
 
+def _scan_fits(c, inputs, cu_seqlens, grads=(None,) * 8, states=(), tokens=()):
+    """Sizes, types and devices of the tensors behind a call's arguments (the kernels know the
+    configuration's)."""
+    x, Bm, Cm, dt, A, D, decay = getattr(inputs, "tensors", (None,) * 7)
+    dx, dBm, dCm, ddt, dlog, dA, dD, dstate = grads
+    _here(x, Bm, Cm, dt, A, D, decay, cu_seqlens, *grads, *states, *tokens)
+    for name, t, row in (("x", x, c.heads * c.dv), ("Bm", Bm, c.ngroups * c.dk), ("Cm", Cm, c.ngroups * c.dk)):
+        if t is not None and hasattr(t, "numel") and t.numel() != t.shape[0] * row:
+            raise ValueError("%s: expected %d elements a token, got %s" % (name, row, tuple(t.shape)))
+    _sized(c.tokens * c.heads * c.dv, RSQ_BF16, x=x, dx=dx, **{"out": t for t in tokens})
+    _sized(c.tokens * c.ngroups * c.dk, RSQ_BF16, Bm=Bm, Cm=Cm, dBm=dBm, dCm=dCm)
+    _sized(c.tokens * c.heads, RSQ_F32, dt=dt, decay=decay, ddt=ddt, dlog_decay=dlog)
+    _sized(c.heads, RSQ_F32, A=A, D=D, dA=dA, dD=dD)
+    for t in states + (dstate,):
+        _sized(c.sequences * c.heads * c.dk * c.dv, RSQ_F32, state=t)
+    _sized(c.sequences + 1, "int32", cu_seqlens=cu_seqlens)
+
+
 def rsq_scan(cfg: rsq_scan_config, inputs: rsq_scan_inputs, out, *, cu_seqlens=None, state_in=None,
              state_out=None, workspace=None, stream=None) -> None:
+    _scan_fits(cfg, inputs, cu_seqlens, states=(state_in, state_out), tokens=(out,))
     ws, n = _workspace(workspace)
     _check(lib.rsq_scan(ctypes.byref(cfg), ctypes.byref(inputs), _dptr(cu_seqlens), _dptr(state_in),
                         _dptr(state_out), _dptr(out), ws, n, _stream(stream)))
@@ -512,6 +531,7 @@ def rsq_scan(cfg: rsq_scan_config, inputs: rsq_scan_inputs, out, *, cu_seqlens=N
 
 def rsq_scan_backward(cfg: rsq_scan_config, inputs: rsq_scan_inputs, dout, grads: rsq_scan_grads, *,
                       cu_seqlens=None, state_in=None, dstate_out=None, workspace=None, stream=None) -> None:
+    _scan_fits(cfg, inputs, cu_seqlens, getattr(grads, "tensors", (None,) * 8), (state_in, dstate_out), (dout,))
     ws, n = _workspace(workspace)
     _check(lib.rsq_scan_backward(ctypes.byref(cfg), ctypes.byref(inputs), _dptr(cu_seqlens), _dptr(state_in),
                                  _dptr(dout), _dptr(dstate_out), ctypes.byref(grads), ws, n, _stream(stream)))
@@ -728,32 +748,12 @@ class Scan:
         n = self.backward_workspace_bytes if backward else self.workspace_bytes
         return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
-    def _fits(self, inputs, cu_seqlens, grads=(None,) * 8, states=(), tokens=()):
-        """Sizes, types and devices of the tensors behind a call's arguments (the kernels know the
-        configuration's)."""
-        c = self.cfg
-        x, Bm, Cm, dt, A, D, decay = getattr(inputs, "tensors", (None,) * 7)
-        dx, dBm, dCm, ddt, dlog, dA, dD, dstate = grads
-        _here(x, Bm, Cm, dt, A, D, decay, cu_seqlens, *grads, *states, *tokens)
-        for name, t, row in (("x", x, c.heads * c.dv), ("Bm", Bm, c.ngroups * c.dk), ("Cm", Cm, c.ngroups * c.dk)):
-            if t is not None and hasattr(t, "numel") and t.numel() != t.shape[0] * row:
-                raise ValueError("%s: expected %d elements a token, got %s" % (name, row, tuple(t.shape)))
-        _sized(c.tokens * c.heads * c.dv, RSQ_BF16, x=x, dx=dx, **{"out": t for t in tokens})
-        _sized(c.tokens * c.ngroups * c.dk, RSQ_BF16, Bm=Bm, Cm=Cm, dBm=dBm, dCm=dCm)
-        _sized(c.tokens * c.heads, RSQ_F32, dt=dt, decay=decay, ddt=ddt, dlog_decay=dlog)
-        _sized(c.heads, RSQ_F32, A=A, D=D, dA=dA, dD=dD)
-        for t in states + (dstate,):
-            _sized(c.sequences * c.heads * c.dk * c.dv, RSQ_F32, state=t)
-        _sized(c.sequences + 1, "int32", cu_seqlens=cu_seqlens)
-
     def forward(self, inputs, out, *, state_in=None, state_out=None, cu_seqlens=None, workspace=None, stream=None):
-        self._fits(inputs, cu_seqlens, states=(state_in, state_out), tokens=(out,))
         rsq_scan(self.cfg, inputs, out, cu_seqlens=cu_seqlens, state_in=state_in, state_out=state_out,
                  workspace=workspace, stream=stream)
 
     def backward(self, inputs, dout, grads, *, state_in=None, dstate_out=None, cu_seqlens=None, workspace=None,
                  stream=None):
-        self._fits(inputs, cu_seqlens, getattr(grads, "tensors", (None,) * 8), (state_in, dstate_out), (dout,))
         rsq_scan_backward(self.cfg, inputs, dout, grads, cu_seqlens=cu_seqlens, state_in=state_in,
                           dstate_out=dstate_out, workspace=workspace, stream=stream)
 

@@ -292,3 +292,20 @@ def test_host_tensors_and_what_is_no_tensor_are_refused(calls):
             with pytest.raises(ValueError):
                 call(cfg, **(a | {name: torch.empty(t.shape, dtype=t.dtype)}))
     assert not calls.names
+
+
+def test_the_functions_check_as_the_class_does(calls):
+    cfg, ins, out, state = scan_of().cfg, rsq.scan_inputs(**tokens()), on(T, H, D, dtype=BF), on(2, H, N, D)
+    for kw in [dict(out=on(T - 1, H, D, dtype=BF)), dict(state_in=on(1, H, N, D)), dict(state_out=on(1, H, N, D)),
+               dict(inputs=rsq.scan_inputs(**tokens(dt=on(T, 1)))), dict(cu_seqlens=on(2, dtype=torch.int32))]:
+        with pytest.raises(ValueError):
+            rsq.rsq_scan(cfg, **(dict(inputs=ins, out=out) | kw))
+    for kw in [dict(dout=on(T - 1, H, D, dtype=BF)), dict(grads=rsq.scan_grads(dA=on(1))), dict(dstate_out=on(1, H, N, D)),
+               dict(inputs=rsq.scan_inputs(**tokens(Bm=on(1, G, N, dtype=BF))))]:
+        with pytest.raises(ValueError):
+            rsq.rsq_scan_backward(cfg, **(dict(inputs=ins, dout=out, grads=rsq.scan_grads()) | kw))
+    assert not calls.names
+    rsq.rsq_scan(cfg, ins, out, state_in=state)
+    rsq.rsq_scan(cfg, rsq.rsq_scan_inputs(P, P, P, P, P, None, None, 0, 0, 0), P)     # addresses alone
+    rsq.rsq_scan_backward(cfg, ins, out, rsq.rsq_scan_grads(dx=P), state_in=state)
+    assert calls.names == ["rsq_scan", "rsq_scan", "rsq_scan_backward"]
