@@ -56,13 +56,15 @@ struct NormParams {
     float* part_s;                // [gridDim.x][width] partial dscale, or null
 };
 
-// VEC consecutive elements of type T, as loaded.
+// VEC consecutive elements of type T, as loaded.  load_fixed is for what nothing writes
+// while the kernel runs (a read-only load); load for what the call may write in place.
 template <class T, int VEC>
 struct Raw;
 template <>
 struct Raw<__nv_bfloat16, 8> {
     uint4 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void load_fixed(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
     __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ float get(int i) const {
         const uint32_t w = i < 2 ? v.x : (i < 4 ? v.y : (i < 6 ? v.z : v.w));
@@ -73,6 +75,10 @@ template <>
 struct Raw<float, 8> {
     float4 a, b;
     __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void load_fixed(const float* p) {
         a = __ldg(reinterpret_cast<const float4*>(p));
         b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     }
@@ -93,14 +99,16 @@ struct Raw<float, 8> {
 template <>
 struct Raw<__nv_bfloat16, 1> {
     unsigned short v;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const unsigned short*>(p)); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const unsigned short*>(p); }
+    __device__ __forceinline__ void load_fixed(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const unsigned short*>(p)); }
     __device__ __forceinline__ void zero() { v = 0; }
     __device__ __forceinline__ float get(int) const { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 };
 template <>
 struct Raw<float, 1> {
     float v;
-    __device__ __forceinline__ void load(const float* p) { v = __ldg(p); }
+    __device__ __forceinline__ void load(const float* p) { v = *p; }
+    __device__ __forceinline__ void load_fixed(const float* p) { v = __ldg(p); }
     __device__ __forceinline__ void zero() { v = 0.f; }
     __device__ __forceinline__ float get(int) const { return v; }
 };
@@ -133,7 +141,7 @@ __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[VEC]) {
 template <int VEC>
 __device__ __forceinline__ void load_cols(const float* p, float (&v)[VEC]) {
     Raw<float, VEC> r;
-    r.load(p);
+    r.load_fixed(p);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) v[i] = r.get(i);
 }
@@ -174,12 +182,17 @@ struct Part {
     Raw<T, VEC> v[K];
 
     // `mine`: the thread's first vector, the others `apart` elements from one another; zero
-    // where not `on`
-    __device__ __forceinline__ void fetch(const T* mine, int apart, const bool (&on)[K], bool row_on) {
+    // where not `on`.  `fixed`: no call may write the array in place
+    __device__ __forceinline__ void fetch(const T* mine, int apart, const bool (&on)[K], bool row_on, bool fixed) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             v[k].zero();
-            if (on[k] && row_on) v[k].load(mine + k * apart);
+            if (on[k] && row_on) {
+                if (fixed)
+                    v[k].load_fixed(mine + k * apart);
+                else
+                    v[k].load(mine + k * apart);
+            }
         }
     }
 };
@@ -202,8 +215,8 @@ norm_kernel(const __grid_constant__ NormParams p) {
         const bool row_on = row < p.rows;
         Part<TX, VEC, K> xs;
         Part<TS, VEC, K> ss;
-        xs.fetch(x + row * p.xs + col, apart, on, row_on);
-        if constexpr (MODE != kPlain) ss.fetch(side + row * p.ss + col, apart, on, row_on && side);
+        xs.fetch(x + row * p.xs + col, apart, on, row_on, true);
+        if constexpr (MODE != kPlain) ss.fetch(side + row * p.ss + col, apart, on, row_on && side, MODE != kResidual);  // h over the residual
         float u[K][VEC];
         float sum = 0.f;
 #pragma unroll
@@ -351,10 +364,10 @@ norm_backward_kernel(const __grid_constant__ NormParams p) {
         Part<TX, VEC, K> xs;
         Part<TS, VEC, K> ss, hs;
         Part<TY, VEC, K> ys;
-        ys.fetch(static_cast<const TY*>(p.dy) + packed, apart, on, row_on);
-        if (MODE != kResidual || want_s) xs.fetch(x + row * p.xs + col, apart, on, row_on);
-        if constexpr (MODE != kPlain) ss.fetch(side + row * p.ss + col, apart, on, row_on);
-        if constexpr (MODE == kResidual) hs.fetch(dh + packed, apart, on, row_on && dh);
+        ys.fetch(static_cast<const TY*>(p.dy) + packed, apart, on, row_on, true);
+        if (MODE != kResidual || want_s) xs.fetch(x + row * p.xs + col, apart, on, row_on, true);
+        if constexpr (MODE != kPlain) ss.fetch(side + row * p.ss + col, apart, on, row_on, true);
+        if constexpr (MODE == kResidual) hs.fetch(dh + packed, apart, on, row_on && dh, false);  // dresidual over dh
 
         float sg[K][VEC], w[VEC] = {};
         // u: what is normed; dn: the gradient of n
@@ -461,7 +474,7 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* part_w, c
     const int lane = threadIdx.x & 31, q = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < width)
-        for (int i = q; i < parts; i += 32) s += __ldg(part + static_cast<long long>(i) * width + c);
+        for (int i = q; i < parts; i += 32) s += part[static_cast<long long>(i) * width + c];
     sh[q][lane] = s;
     __syncthreads();
     if (q == 0 && c < width) {

@@ -23,8 +23,8 @@ template <int R, int TERMS>
 __device__ __forceinline__ void load_state(uint32_t dst, const float* src) {
     for (int i = threadIdx.x; i < R * 8; i += kThreads) {
         const int r = i >> 3, c = i & 7;
-        const float4 a = __ldg(reinterpret_cast<const float4*>(src + r * kTile + c * 8));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(src + r * kTile + c * 8) + 1);
+        const float4 a = *reinterpret_cast<const float4*>(src + r * kTile + c * 8);
+        const float4 b = *(reinterpret_cast<const float4*>(src + r * kTile + c * 8) + 1);
         uint32_t t[3][4];
         split3(a.x, a.y, t[0][0], t[1][0], t[2][0]);
         split3(a.z, a.w, t[0][1], t[1][1], t[2][1]);
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
                 const float* ds = p.df + cell + part * Sh::kRows * kTile;
                 load_state<Sh::kRows, 3>(sp, s0);
                 for (int i = threadIdx.x; i < Sh::kRows * kTile / 4; i += kThreads) {
-                    const float4 u = __ldg(reinterpret_cast<const float4*>(s0) + i), v = __ldg(reinterpret_cast<const float4*>(ds) + i);
+                    const float4 u = reinterpret_cast<const float4*>(s0)[i], v = reinterpret_cast<const float4*>(ds)[i];
                     through = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, through))));
                 }
                 __syncthreads();

@@ -8,6 +8,9 @@
 // complete kernel always means that those before it are complete as well.  The first
 // kernel of a call starts after all that is in the stream.
 //
+// What a kernel of the same call writes is read by plain loads: its writer may still run
+// when the reader's blocks start, and a read-only load (__ldg) may be moved over the wait.
+//
 // Kernels of several rounds of blocks do not call let_next(): with the next kernel's
 // blocks placed while the last round ran, the gradient of 4 x 2048 tokens with 80 heads of
 // 128 x 64 took 593 us instead of 562.  Against plain launches: that gradient 575 -> 562 us, the

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const float* src = ps.local ? nullptr : (p.seg_chunks ? p.seg_start[ps.rev] + seg_at : (init ? init + at0 : nullptr));
-            S[i] = src ? __ldg(src + static_cast<long long>(i) * p.P) : 0.f;
+            S[i] = src ? src[static_cast<long long>(i) * p.P] : 0.f;
         }
         const long long gate_at = (static_cast<long long>(slot0) * p.H + h) * kChunk + kChunk - 1;
         bool ok = true;
