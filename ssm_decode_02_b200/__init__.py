@@ -208,22 +208,10 @@ def _dptr(t) -> int | None:
     return int(t.data_ptr())
 
 
-def _dptr_rows(t) -> int | None:
-    """As _dptr, for an argument whose rows may lie apart: only its last dimension
-    has to be contiguous."""
-    if t is None or isinstance(t, int) or not hasattr(t, "data_ptr") or not getattr(t, "is_cuda", False):
-        return _dptr(t)
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError("expected a CUDA tensor with a contiguous last dimension")
-    return int(t.data_ptr())
-
-
 def _workspace(t) -> tuple[int | None, int]:
     if t is None:
         return None, 0
-    p = _dptr(t)
-    _here(t)
-    return p, t.numel() * t.element_size()
+    return _arg(t, 0, None, _device(), "workspace"), t.numel() * t.element_size()
 
 
 def _current_device() -> int:
@@ -246,21 +234,76 @@ def _types() -> dict:
     return _torch_types
 
 
-def _sized(count: int, type_, **tensors) -> None:
-    """Refuses tensors of fewer than count elements, or of another type than type_ (a key of
-    _types; others are the library's to refuse): the kernels take sizes and types from the
-    configuration alone, and read float16 bits as bfloat16.  Addresses pass."""
-    want = _types().get(type_)
-    for name, t in tensors.items():
-        if t is not None and hasattr(t, "numel") and (t.numel() < count or (t.dtype is not want and want is not None)):
-            raise ValueError("%s: expected at least %d elements of %s, got %s of %s" % (name, count, want, tuple(t.shape), t.dtype))
+def _device() -> int | None:
+    """The current device; None without one, so that no tensor is on it."""
+    try:
+        return _current_device()
+    except (RuntimeError, AssertionError):
+        return None
 
 
-def _here(*tensors) -> None:
-    """Refuses tensors of another GPU than the current one, whose stream the call uses."""
-    for t in tensors:
-        if t is not None and getattr(t, "is_cuda", False) and t.get_device() != _current_device():
-            raise ValueError("a tensor is on cuda:%d, the current device is cuda:%d" % (t.get_device(), _current_device()))
+def _refuse(t, count: int, want, name: str) -> None:
+    """Says what is wrong with an argument that _arg does not take."""
+    if not hasattr(t, "data_ptr"):
+        raise TypeError("%s: expected a CUDA tensor, got %r" % (name, type(t)))
+    if not t.is_cuda:
+        raise ValueError("%s: expected a CUDA tensor, got one on %s" % (name, t.device))
+    if t.numel() < count or (want is not None and t.dtype is not want):
+        raise ValueError("%s: expected at least %d elements of %s, got %s of %s" % (name, count, want, tuple(t.shape), t.dtype))
+    raise ValueError("%s is on cuda:%d, the current device is cuda:%s" % (name, t.get_device(), _device()))
+
+
+def _fits(t, count: int, want, here, name: str) -> None:
+    """Refuses a tensor of fewer than count elements, of another type than want (None: the
+    library's to refuse) or of another GPU than `here`, whose stream the call uses: the kernels
+    take sizes and types from the configuration alone, and read float16 bits as bfloat16.
+    Addresses pass."""
+    if t is None or isinstance(t, int):
+        return
+    try:
+        if t.numel() >= count and (t.dtype is want or want is None) and t.get_device() == here:
+            return
+    except AttributeError:
+        pass
+    _refuse(t, count, want, name)
+
+
+def _arg(t, count: int, want, here, name: str) -> int | None:
+    """_fits, and the address of a contiguous tensor."""
+    if t is None or isinstance(t, int):
+        return t
+    try:
+        if t.numel() >= count and (t.dtype is want or want is None) and t.get_device() == here and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    p = _dptr(t)
+    _refuse(t, count, want, name)
+    return p
+
+
+def _arg_rows(t, rows: int, width: int, stride: int, want, here, name: str) -> int | None:
+    """As _arg, for rows that may lie apart: as `stride` (0: packed) says, since the kernels go by
+    the configuration, whichever tensors it was made from."""
+    if t is None or isinstance(t, int):
+        return t
+    if (stride == width or not stride) and hasattr(t, "is_contiguous") and t.is_contiguous():
+        return _arg(t, rows * width, want, here, name)
+    _fits(t, rows * width, want, here, name)
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("%s: expected a contiguous last dimension" % name)
+    if rows > 1:
+        stride, inner = stride or width, 1
+        for d in range(t.dim() - 1, 0, -1):     # the columns of a row, as far as they are packed
+            if t.shape[d] > 1 and t.stride(d) != inner:
+                break
+            inner *= t.shape[d]
+        else:
+            if t.dim() > 1 and t.stride(0) == stride and t.shape[0] >= rows and inner >= width:
+                return t.data_ptr()
+        raise ValueError("%s: the configuration has %d rows of %d columns, %d elements apart; got shape %s with strides %s"
+                         % (name, rows, width, stride, tuple(t.shape), tuple(t.stride())))
+    return t.data_ptr()
 
 
 def _dtype_of(t) -> int:
@@ -503,38 +546,46 @@ def rsq_scan_workspace(cfg: rsq_scan_config, backward: bool = False) -> int:
     return int(n.value)
 
 
-def _scan_fits(c, inputs, cu_seqlens, grads=(None,) * 8, states=(), tokens=()):
-    """Sizes, types and devices of the tensors behind a call's arguments (the kernels know the
-    configuration's)."""
+def _scan_args(c, inputs, out, cu_seqlens, states, grads=None) -> list:
+    """Checks the tensors behind a call's arguments, whose sizes, types and device the kernels
+    take from the configuration; the addresses of cu_seqlens, the states and out."""
+    types, here = _types(), _device()
+    f32, bf16 = types[RSQ_F32], types[RSQ_BF16]
+    tokens, gates = c.tokens, c.tokens * c.heads
+    x_row, b_row = c.heads * c.dv, c.ngroups * c.dk
     x, Bm, Cm, dt, A, D, decay = getattr(inputs, "tensors", (None,) * 7)
-    dx, dBm, dCm, ddt, dlog, dA, dD, dstate = grads
-    _here(x, Bm, Cm, dt, A, D, decay, cu_seqlens, *grads, *states, *tokens)
-    for name, t, row in (("x", x, c.heads * c.dv), ("Bm", Bm, c.ngroups * c.dk), ("Cm", Cm, c.ngroups * c.dk)):
-        if t is not None and hasattr(t, "numel") and t.numel() != t.shape[0] * row:
-            raise ValueError("%s: expected %d elements a token, got %s" % (name, row, tuple(t.shape)))
-    _sized(c.tokens * c.heads * c.dv, RSQ_BF16, x=x, dx=dx, **{"out": t for t in tokens})
-    _sized(c.tokens * c.ngroups * c.dk, RSQ_BF16, Bm=Bm, Cm=Cm, dBm=dBm, dCm=dCm)
-    _sized(c.tokens * c.heads, RSQ_F32, dt=dt, decay=decay, ddt=ddt, dlog_decay=dlog)
-    _sized(c.heads, RSQ_F32, A=A, D=D, dA=dA, dD=dD)
-    for t in states + (dstate,):
-        _sized(c.sequences * c.heads * c.dk * c.dv, RSQ_F32, state=t)
-    _sized(c.sequences + 1, "int32", cu_seqlens=cu_seqlens)
+    for name, t, row in (("x", x, x_row), ("Bm", Bm, b_row), ("Cm", Cm, b_row)):
+        if t is not None and not isinstance(t, int):
+            _fits(t, tokens * row, bf16, here, name)
+            if t.numel() != t.shape[0] * row:
+                raise ValueError("%s: expected %d elements a token, got %s" % (name, row, tuple(t.shape)))
+    rest = [("dt", dt, gates, f32), ("decay", decay, gates, f32), ("A", A, c.heads, f32), ("D", D, c.heads, f32)]
+    state = c.sequences * x_row * c.dk
+    if grads is not None:
+        dx, dBm, dCm, ddt, dlog, dA, dD, dstate = getattr(grads, "tensors", (None,) * 8)
+        rest += [("dx", dx, tokens * x_row, bf16), ("dBm", dBm, tokens * b_row, bf16), ("dCm", dCm, tokens * b_row, bf16),
+                 ("ddt", ddt, gates, f32), ("dlog_decay", dlog, gates, f32), ("dA", dA, c.heads, f32), ("dD", dD, c.heads, f32),
+                 ("dstate_in", dstate, state, f32)]
+    for name, t, count, want in rest:
+        if t is not None:
+            _fits(t, count, want, here, name)
+    return [_arg(cu_seqlens, c.sequences + 1, types["int32"], here, "cu_seqlens"), _arg(states[0], state, f32, here, "state_in"),
+            _arg(states[1], state, f32, here, "the second state"), _arg(out, tokens * x_row, bf16, here, "out or dout")]
 
 
 def rsq_scan(cfg: rsq_scan_config, inputs: rsq_scan_inputs, out, *, cu_seqlens=None, state_in=None,
              state_out=None, workspace=None, stream=None) -> None:
-    _scan_fits(cfg, inputs, cu_seqlens, states=(state_in, state_out), tokens=(out,))
+    cu, first, last, to = _scan_args(cfg, inputs, out, cu_seqlens, (state_in, state_out))
     ws, n = _workspace(workspace)
-    _check(lib.rsq_scan(ctypes.byref(cfg), ctypes.byref(inputs), _dptr(cu_seqlens), _dptr(state_in),
-                        _dptr(state_out), _dptr(out), ws, n, _stream(stream)))
+    _check(lib.rsq_scan(ctypes.byref(cfg), ctypes.byref(inputs), cu, first, last, to, ws, n, _stream(stream)))
 
 
 def rsq_scan_backward(cfg: rsq_scan_config, inputs: rsq_scan_inputs, dout, grads: rsq_scan_grads, *,
                       cu_seqlens=None, state_in=None, dstate_out=None, workspace=None, stream=None) -> None:
-    _scan_fits(cfg, inputs, cu_seqlens, getattr(grads, "tensors", (None,) * 8), (state_in, dstate_out), (dout,))
+    cu, first, last, given = _scan_args(cfg, inputs, dout, cu_seqlens, (state_in, dstate_out), grads)
     ws, n = _workspace(workspace)
-    _check(lib.rsq_scan_backward(ctypes.byref(cfg), ctypes.byref(inputs), _dptr(cu_seqlens), _dptr(state_in),
-                                 _dptr(dout), _dptr(dstate_out), ctypes.byref(grads), ws, n, _stream(stream)))
+    _check(lib.rsq_scan_backward(ctypes.byref(cfg), ctypes.byref(inputs), cu, first, given, last, ctypes.byref(grads), ws, n,
+                                 _stream(stream)))
 
 
 def rsq_scan_check(workspace, stream=None) -> None:
@@ -551,92 +602,45 @@ def rsq_norm_workspace(cfg: rsq_norm_config) -> int:
     return int(n.value)
 
 
-def _norm_sized(cfg, x, side, y, w) -> None:
-    """As _sized and _here for what every norm call has, without keywords: a decode step's call
-    takes a few microseconds in all."""
-    n, types = cfg.rows * cfg.width, _types()
-    for t, count, type_ in ((x, n, cfg.x_dtype), (side, n, cfg.side_dtype), (y, n, cfg.y_dtype), (w, cfg.width, RSQ_F32)):
-        if t is None or not hasattr(t, "numel"):
-            continue
-        want = types.get(type_)        # None: the library's to refuse
-        if t.numel() < count or (t.dtype is not want and want is not None):
-            raise ValueError("expected %d rows of %d columns in the configuration's types, got %s of %s"
-                             % (cfg.rows, cfg.width, tuple(t.shape), t.dtype))
-    _here(x, side, y, w)
-
-
-def _rows_as(t, rows: int, width: int, stride: int, what: str) -> None:
-    """Refuses a tensor whose rows lie other than `stride` (0: packed) says: the kernels go by the
-    configuration, whichever tensors it was made from."""
-    if t is None or isinstance(t, int) or rows < 2:
-        return
-    stride = stride or width
-    dim = t.dim()
-    if dim > 1 and t.stride(0) == stride and t.shape[0] >= rows:
-        if dim == 2 and t.shape[1] >= width:
-            return
-        inner = 1
-        for d in range(dim - 1, 0, -1):
-            if t.shape[d] > 1 and t.stride(d) != inner:
-                break
-            inner *= t.shape[d]
-        else:
-            if inner >= width:
-                return
-    if stride == width and t.is_contiguous():
-        return
-    raise ValueError("%s: the configuration has %d rows of %d columns, %d elements apart; got shape %s with strides %s"
-                     % (what, rows, width, stride, tuple(t.shape), tuple(t.stride())))
-
-
 def rsq_gated_norm(cfg: rsq_norm_config, x, z, w, y, stream=None) -> None:
     """x and z may be row-strided, as the configuration says (norm_config reads their strides)."""
-    _norm_sized(cfg, x, z, y, w)
-    _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
-    _rows_as(z, cfg.rows, cfg.width, cfg.side_stride, "z")
-    _check(lib.rsq_gated_norm(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(z), _dptr(w), _dptr(y),
-                              _stream(stream)))
+    types, here, rows, width = _types(), _device(), cfg.rows, cfg.width
+    args = (_arg_rows(x, rows, width, cfg.x_stride, types.get(cfg.x_dtype), here, "x"),
+            _arg_rows(z, rows, width, cfg.side_stride, types.get(cfg.side_dtype), here, "z"),
+            _arg(w, width, types[RSQ_F32], here, "w"), _arg(y, rows * width, types.get(cfg.y_dtype), here, "y"))
+    _check(lib.rsq_gated_norm(ctypes.byref(cfg), *args, _stream(stream)))
 
 
 def rsq_gated_norm_backward(cfg: rsq_norm_config, x, z, w, dy, dx, dz, dw, workspace=None, stream=None) -> None:
-    _norm_sized(cfg, x, z, dy, w)
-    _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
-    _rows_as(z, cfg.rows, cfg.width, cfg.side_stride, "z")
-    _sized(cfg.rows * cfg.width, cfg.x_dtype, dx=dx)
-    _sized(cfg.rows * cfg.width, cfg.side_dtype, dz=dz)
-    _sized(cfg.width, RSQ_F32, dw=dw)
-    _here(dx, dz, dw)
-    ws, n = _workspace(workspace)
-    _check(lib.rsq_gated_norm_backward(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(z), _dptr(w), _dptr(dy),
-                                       _dptr(dx), _dptr(dz), _dptr(dw), ws, n, _stream(stream)))
+    types, here, rows, width = _types(), _device(), cfg.rows, cfg.width
+    n, tx, ts, f32 = rows * width, types.get(cfg.x_dtype), types.get(cfg.side_dtype), types[RSQ_F32]
+    ws, ws_bytes = _workspace(workspace)
+    args = (_arg_rows(x, rows, width, cfg.x_stride, tx, here, "x"), _arg_rows(z, rows, width, cfg.side_stride, ts, here, "z"),
+            _arg(w, width, f32, here, "w"), _arg(dy, n, types.get(cfg.y_dtype), here, "dy"), _arg(dx, n, tx, here, "dx"),
+            _arg(dz, n, ts, here, "dz"), _arg(dw, width, f32, here, "dw"), ws, ws_bytes)
+    _check(lib.rsq_gated_norm_backward(ctypes.byref(cfg), *args, _stream(stream)))
 
 
 def rsq_residual_norm(cfg: rsq_norm_config, x, residual, scale, w, h, y, stream=None) -> None:
     """x and residual may be row-strided, as the configuration says (norm_config reads their strides)."""
-    _norm_sized(cfg, x, residual, y, w)
-    _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
-    _rows_as(residual, cfg.rows, cfg.width, cfg.side_stride, "residual")
-    if h is not residual:
-        _sized(cfg.rows * cfg.width, cfg.side_dtype, h=h)
-    if scale is not None:
-        _sized(cfg.width, RSQ_F32, scale=scale)
-    _here(h, scale)
-    _check(lib.rsq_residual_norm(ctypes.byref(cfg), _dptr_rows(x), _dptr_rows(residual), _dptr(scale), _dptr(w),
-                                 _dptr(h), _dptr(y), _stream(stream)))
+    types, here, rows, width = _types(), _device(), cfg.rows, cfg.width
+    n, ts, f32 = rows * width, types.get(cfg.side_dtype), types[RSQ_F32]
+    args = (_arg_rows(x, rows, width, cfg.x_stride, types.get(cfg.x_dtype), here, "x"),
+            _arg_rows(residual, rows, width, cfg.side_stride, ts, here, "residual"), _arg(scale, width, f32, here, "scale"),
+            _arg(w, width, f32, here, "w"), _arg(h, n, ts, here, "h"), _arg(y, n, types.get(cfg.y_dtype), here, "y"))
+    _check(lib.rsq_residual_norm(ctypes.byref(cfg), *args, _stream(stream)))
 
 
 def rsq_residual_norm_backward(cfg: rsq_norm_config, x, h, scale, w, dy, dh, dx, dresidual, dscale, dw,
                                workspace=None, stream=None) -> None:
-    _norm_sized(cfg, x, h, dy, w)
-    _rows_as(x, cfg.rows, cfg.width, cfg.x_stride, "x")
-    _sized(cfg.rows * cfg.width, cfg.side_dtype, dh=dh, dresidual=dresidual)
-    _sized(cfg.rows * cfg.width, cfg.x_dtype, dx=dx)
-    _sized(cfg.width, RSQ_F32, scale=scale, dw=dw, dscale=dscale)
-    _here(dh, dx, dresidual, scale, dw, dscale)
-    ws, n = _workspace(workspace)
-    _check(lib.rsq_residual_norm_backward(ctypes.byref(cfg), _dptr_rows(x), _dptr(h), _dptr(scale), _dptr(w),
-                                          _dptr(dy), _dptr(dh), _dptr(dx), _dptr(dresidual), _dptr(dscale),
-                                          _dptr(dw), ws, n, _stream(stream)))
+    types, here, rows, width = _types(), _device(), cfg.rows, cfg.width
+    n, tx, ts, f32 = rows * width, types.get(cfg.x_dtype), types.get(cfg.side_dtype), types[RSQ_F32]
+    ws, ws_bytes = _workspace(workspace)
+    args = (_arg_rows(x, rows, width, cfg.x_stride, tx, here, "x"), _arg(h, n, ts, here, "h"), _arg(scale, width, f32, here, "scale"),
+            _arg(w, width, f32, here, "w"), _arg(dy, n, types.get(cfg.y_dtype), here, "dy"), _arg(dh, n, ts, here, "dh"),
+            _arg(dx, n, tx, here, "dx"), _arg(dresidual, n, ts, here, "dresidual"), _arg(dscale, width, f32, here, "dscale"),
+            _arg(dw, width, f32, here, "dw"), ws, ws_bytes)
+    _check(lib.rsq_residual_norm_backward(ctypes.byref(cfg), *args, _stream(stream)))
 
 
 def rsq_version() -> str:
@@ -704,8 +708,11 @@ def scan_inputs(x, Bm, Cm, dt=None, A=None, D=None, decay=None) -> rsq_scan_inpu
     """x [tokens, heads, dv], Bm, Cm [tokens, ngroups, dk]: their tokens may lie apart.  The
     result keeps the tensors that it points at."""
     (xp, xs), (bp, bs), (cp, cs) = _token_rows(x, "x"), _token_rows(Bm, "Bm"), _token_rows(Cm, "Cm")
-    _sized(0, RSQ_BF16, x=x, Bm=Bm, Cm=Cm)
-    _sized(0, RSQ_F32, dt=dt, A=A, D=D, decay=decay)
+    types = _types()
+    for name, t, type_ in (("x", x, RSQ_BF16), ("Bm", Bm, RSQ_BF16), ("Cm", Cm, RSQ_BF16), ("dt", dt, RSQ_F32), ("A", A, RSQ_F32),
+                           ("D", D, RSQ_F32), ("decay", decay, RSQ_F32)):
+        if t is not None and not isinstance(t, int) and t.dtype is not types[type_]:
+            raise ValueError("%s: expected %s, got %s" % (name, types[type_], t.dtype))
     ins = rsq_scan_inputs(xp, bp, cp, _dptr(dt), _dptr(A), _dptr(D), _dptr(decay), xs, bs, cs)
     ins.tensors = (x, Bm, Cm, dt, A, D, decay)
     return ins
