@@ -1,0 +1,124 @@
+"""Paths of the scan that its other tests do not take: ragged batches in segments, token
+rows that lie apart on the tensor-map path, strong decays in the tcgen05 gradient, states in
+place.  References and tolerances are those of test_gpu_scan.py."""
+import pytest
+import torch
+
+import ssm_decode_02_b200 as rsq
+from test_gpu_scan import check_backward, check_forward, cuda, inputs, make, poison, reference_grads, shape
+
+pytestmark = pytest.mark.gpu
+
+
+def run(d, bounds, *, ragged, apart=False, in_place=False, dout=None, dstate=None):
+    """(out, state_out, gradients): forward and, with dout, backward.  Rows of no sequence hold NaN.
+    apart: x, B and C are slices of one array whose other columns hold NaN."""
+    c, n = cuda(d), len(bounds) - 1
+    T, H, P = d["x"].shape
+    G, N = d["Bm"].shape[1:]
+    if apart:
+        wide = torch.full((T, H * P + 2 * G * N + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+        at = [0, H * P + 8, H * P + G * N + 8, H * P + 2 * G * N + 8]
+        for k, lo, hi in (("x", at[0], H * P), ("Bm", at[1], at[2]), ("Cm", at[2], at[3])):
+            wide[:, lo:hi] = c[k].flatten(1)
+            c[k] = wide[:, lo:hi].view(c[k].shape)
+            assert not c[k].is_contiguous()
+    for k in ("x", "Bm", "Cm", "dt", "decay"):
+        if c[k] is not None:
+            c[k][:bounds[0]] = float("nan")
+            c[k][bounds[-1]:] = float("nan")
+    s = shape(d, n, ragged=ragged)
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda") if ragged else None
+    out = torch.full((T, H, P), 7.0, dtype=torch.bfloat16, device="cuda")
+    start = c["state_in"]
+    state = start.clone() if in_place else torch.empty((n, H, N, P), device="cuda")
+    ws = poison(s.alloc_workspace())
+    s.forward(inputs(c), out, state_in=state if in_place else start, state_out=state, cu_seqlens=cu, workspace=ws)
+    rsq.rsq_scan_check(ws)
+    if dout is None:
+        return out.cpu(), state.cpu(), None
+    full = lambda t: torch.full(t.shape, 7.0, dtype=t.dtype, device="cuda")  # noqa: E731
+    g = {"dx": full(d["x"]), "dBm": full(d["Bm"]), "dCm": full(d["Cm"]), "dlog_decay": torch.full((T, H), 7.0, device="cuda"),
+         "dstate_in": dstate.cuda() if in_place else torch.empty((n, H, N, P), device="cuda")}
+    if d["decay"] is None:
+        g |= {"ddt": full(d["dt"]), "dA": full(d["A"])}
+    if d["D"] is not None:
+        g["dD"] = full(d["D"])
+    doutc = dout.cuda()
+    doutc[:bounds[0]] = float("nan")
+    doutc[bounds[-1]:] = float("nan")
+    bws = poison(s.alloc_workspace(backward=True))
+    s.backward(inputs(c), doutc, rsq.scan_grads(**g), state_in=start, dstate_out=g["dstate_in"] if in_place else dstate.cuda(),
+               cu_seqlens=cu, workspace=bws)
+    rsq.rsq_scan_check(bws)
+    return out.cpu(), state.cpu(), {k: v.cpu() for k, v in g.items()}
+
+
+def gradients_of(d, n, seed):
+    g = torch.Generator().manual_seed(seed)
+    T, H, P = d["x"].shape
+    return torch.randn(d["x"].shape, generator=g).bfloat16(), torch.randn((n, H, d["Bm"].shape[2], P), generator=g)
+
+
+def check_all(d, bounds, got, dout, dstate):
+    out, state, grads = got
+    check_forward(d, bounds, out, state)
+    check_backward(d, bounds, grads, reference_grads(d, bounds, dout, dstate))
+
+
+# ------------------------------------------------------------------------------------- segments
+def bytes_without_segments(n, T, H, N, P, backward):
+    """The workspace of a ragged call whose sequences are not cut into segments."""
+    slots = T // 128 + n
+    cells, state = slots * H, N * 64 * -(-P // 64)
+    sizes = [4, slots * 8, cells * 128 * 8, cells * 128 * 4]
+    sizes += [cells * state * 4, cells * state * 4, 2 * cells * 4] if backward else [cells * state * 2]
+    return sum(-(-k // 256) * 256 for k in sizes)
+
+
+SEGMENTED = [3, 5603, 5603, 5604, 5613, 9690]    # long, empty, one token, nine tokens, long
+ROWS = 9700
+
+
+def test_the_size_without_segments_is_known():
+    s = rsq.Scan(40, ROWS, 2, 64, 64, ragged=True)     # too many sequences for segments
+    assert s.workspace_bytes == bytes_without_segments(40, ROWS, 2, 64, 64, False)
+    assert s.backward_workspace_bytes == bytes_without_segments(40, ROWS, 2, 64, 64, True)
+
+
+@pytest.mark.parametrize("H,N,P", [(1, 16, 16), (2, 64, 64), (1, 64, 256), (1, 256, 128)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_ragged_batch_in_segments(H, N, P, in_place):
+    n = len(SEGMENTED) - 1
+    s = rsq.Scan(n, ROWS, H, N, P, ragged=True)
+    assert s.workspace_bytes > bytes_without_segments(n, ROWS, H, N, P, False)
+    assert s.backward_workspace_bytes > bytes_without_segments(n, ROWS, H, N, P, True)
+    d, bounds = make(n, ROWS, H, N, P, 1, bounds=SEGMENTED, seed=51)
+    dout, dstate = gradients_of(d, n, 52)
+    check_all(d, bounds, run(d, bounds, ragged=True, in_place=in_place, dout=dout, dstate=dstate), dout, dstate)
+
+
+# --------------------------------------------------------------------------------- rows that lie apart
+@pytest.mark.parametrize("H,N,P,G", [(2, 64, 64, 1), (4, 128, 64, 2), (2, 128, 128, 2), (2, 256, 64, 1), (1, 64, 256, 1)])
+@pytest.mark.parametrize("bounds", [[0, 300, 600], [5, 261, 261, 274, 590]])
+def test_rows_apart_on_tensor_maps(H, N, P, G, bounds):
+    """x, B and C as slices of one projection, as a Mamba-2 layer has them: whole chunks come as
+    tensor-map boxes, the last rows of a sequence by themselves."""
+    n, ragged = len(bounds) - 1, bounds[0] > 0
+    d, bounds = make(n, 600, H, N, P, G, bounds=bounds, seed=61)
+    dout, dstate = gradients_of(d, n, 62)
+    check_all(d, bounds, run(d, bounds, ragged=ragged, apart=True, dout=dout, dstate=dstate), dout, dstate)
+
+
+# --------------------------------------------------------------------------------------- strong decays
+@pytest.mark.parametrize("H,N,P,G", [(4, 64, 64, 1), (4, 128, 64, 2), (3, 128, 128, 3), (2, 256, 64, 1), (2, 64, 256, 1)])
+@pytest.mark.parametrize("decay", [False, True])
+def test_strong_decays_and_restarts_on_tensor_cores(H, N, P, G, decay):
+    """Decays of zero and far below the smallest float within a block of 32 tokens, where the kernels
+    take a power for each pair in the place of two factors."""
+    d, bounds = make(2, 2 * 270, H, N, P, G, decay=decay, strong=True, seed=71)
+    dout, dstate = gradients_of(d, 2, 72)
+    got = run(d, bounds, ragged=False, dout=dout, dstate=dstate)
+    check_all(d, bounds, got, dout, dstate)
+    if decay:
+        assert (d["decay"] == 0).any() and (got[2]["dlog_decay"][d["decay"] == 0] == 0).all()
