@@ -511,7 +511,9 @@ rsq_status rsq_pipe_streams(const rsq_pipe* pipe, void** copy_in, void** compute
  * rsq_scan_check: the scan's kernels wait for their own copies and products with a
  *   limit; a kernel whose wait runs out marks the call's workspace and ends, its
  *   outputs incomplete.  Synchronizes `stream` and returns RSQ_E_CUDA when the last
- *   call with this workspace was so marked, else RSQ_OK.  Not capturable. */
+ *   call with this workspace was so marked, else RSQ_OK.  A call that needs no
+ *   workspace clears the mark of one that it is given (4 bytes or more, 16-byte
+ *   aligned), and touches nothing else of it.  Not capturable. */
 typedef struct {
     int family;
     int in_dtype;

@@ -248,7 +248,11 @@ rsq_status rsq_scan(const rsq_scan_config* cfg, const rsq_scan_inputs* inputs, c
     p.state_out = state_out;
     p.out = static_cast<bf16*>(out);
     auto s = static_cast<cudaStream_t>(stream);
-    if (steps) return done("scan", launch_step(p, s));
+    if (steps) {
+        // needs no workspace, but its mark speaks of the last call with it (rsq_scan_check)
+        if (workspace && !misaligned(workspace) && workspace_bytes >= sizeof(unsigned)) p.flag = static_cast<unsigned*>(workspace);
+        return done("scan", launch_step(p, s));
+    }
     if (cfg->ragged) {
         p.steps = kStepTokens;
         const int most = p.tokens / (kStepTokens + 1);

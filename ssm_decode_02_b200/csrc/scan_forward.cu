@@ -501,6 +501,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const __grid_constant__ 
     __shared__ float key[2][N];                  // B, C of the token
     __shared__ float4 part[kThreads / 32][16];
     wait_before();
+    if (!p.ragged && p.flag && blockIdx.x == 0 && threadIdx.x == 0) *p.flag = 0u;   // a whole call by itself
     const int tile = blockIdx.x % p.tiles, h = (blockIdx.x / p.tiles) % p.H;
     const int seq = blockIdx.x / p.tiles / p.H;
     int lo, len;

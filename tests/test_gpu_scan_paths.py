@@ -122,3 +122,18 @@ def test_strong_decays_and_restarts_on_tensor_cores(H, N, P, G, decay):
     check_all(d, bounds, got, dout, dstate)
     if decay:
         assert (d["decay"] == 0).any() and (got[2]["dlog_decay"][d["decay"] == 0] == 0).all()
+
+
+# ------------------------------------------------------------------------------------------ failure mark
+@pytest.mark.parametrize("tokens", [0, 2, 24])
+def test_a_call_of_single_tokens_clears_the_mark_of_a_workspace_that_it_is_given(tokens):
+    """rsq_scan_check speaks of the last call with the workspace; one that needs none is a call too."""
+    d, bounds = make(2, tokens, 2, 64, 64, 1, seed=81)
+    s, c = shape(d, 2), cuda(d)
+    assert s.alloc_workspace() is None
+    ws = torch.full((1 << 16,), 255, dtype=torch.uint8, device="cuda")   # as an earlier call, or nobody, left it
+    out, state = torch.empty_like(c["x"]), torch.empty_like(c["state_in"])
+    s.forward(inputs(c), out, state_in=c["state_in"], state_out=state, workspace=ws)
+    rsq.rsq_scan_check(ws)
+    check_forward(d, bounds, out.cpu(), state.cpu()) if tokens else None
+    assert torch.equal(ws[4:], torch.full_like(ws[4:], 255))
