@@ -115,7 +115,7 @@ rsq_status check_inputs(const char* who, const rsq_scan_config& c, const rsq_sca
     if (!in) return set_error(RSQ_E_INVAL, "%s: null inputs", who);
     const bool any = c.tokens > 0;
     if (any && (!in->x || !in->Bm || !in->Cm)) return set_error(RSQ_E_INVAL, "%s: null x, Bm or Cm", who);
-    if (!in->decay && (!in->dt || !in->A)) return set_error(RSQ_E_INVAL, "%s: without decay, dt and A are needed", who);
+    if (any && !in->decay && (!in->dt || !in->A)) return set_error(RSQ_E_INVAL, "%s: without decay, dt and A are needed", who);
     if (c.ragged && !cu) return set_error(RSQ_E_INVAL, "%s: ragged needs cu_seqlens", who);
     if (!c.ragged && cu) return set_error(RSQ_E_INVAL, "%s: cu_seqlens without ragged", who);
     for (const void* q : {in->x, in->Bm, in->Cm})
