@@ -581,6 +581,10 @@ rsq_status rsq_scan_check(const void* workspace, void* stream);
  *   x_stride, side_stride: elements between rows of x and of z / residual (0:
  *   width); every other array is packed.
  *   eps > 0.  order: RSQ_NORM_GATE or RSQ_GATE_NORM (residual norm: ignored).
+ * Arrays are 16-byte aligned where width, group and both strides are multiples of
+ * 8 (residual backward: h is packed), else aligned to their elements; the workspace
+ * 16-byte aligned.  No output may overlap an input or another output, but h the
+ * residual and dresidual dh, each whole.
  * Backward passes take what the forward pass read (residual norm: the h it
  * wrote, packed), and write what is not NULL:
  *   gated: dx, dz, dw float [width] (dz must be NULL without z);

@@ -24,6 +24,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "rsq_internal.h"
 #include "scan_launch.cuh"
@@ -490,13 +491,17 @@ struct Geometry {
 // Backward blocks of an SM: those that fit at once (registers), four at most.
 int blocks_fit(const Geometry& g) { return std::max(1, std::min(4, 65536 / (kBackwardRegs * g.tpu * g.upb))); }
 
-// Vectors of eight elements where every row of every array starts on one
-// (width, group and strides multiples of 8; the bases are 16-byte aligned),
-// else single elements.  Two vectors per thread up to groups of 8192, four above:
+// Whether every row of every array starts on a vector of eight elements (the bases are then
+// 16-byte aligned).
+bool is_wide(const rsq_norm_config& c) {
+    return c.group % 8 == 0 && c.width % 8 == 0 && c.x_stride % 8 == 0 && c.side_stride % 8 == 0;
+}
+
+// Vectors of eight elements where rows start on one, else single elements.  Two vectors per thread up to groups of 8192, four above:
 // one would leave half the threads of a block of 512 without work at 5120 columns.
 Geometry geometry(const rsq_norm_config& c, bool backward) {
     Geometry g;
-    const bool wide = c.group % 8 == 0 && c.width % 8 == 0 && c.x_stride % 8 == 0 && c.side_stride % 8 == 0;
+    const bool wide = is_wide(c);
     g.vec = wide ? 8 : 1;
     const int chunks = c.group / g.vec;
     g.k = wide ? (c.group <= 8192 ? 2 : 4) : (c.group <= 8192 ? 16 : 32);
@@ -564,7 +569,21 @@ int launch(int mode, bool backward, const rsq_norm_config& c, const NormParams& 
     }
 }
 
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool misaligned(const void* p, unsigned to = 16) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
+
+// What the arrays of a call have to be aligned to: whole vectors, or single elements.
+unsigned aligned_to(const rsq_norm_config& c, int dtype) { return is_wide(c) ? 16 : (dtype == RSQ_F32 ? 4 : 2); }
+
+struct Array {
+    const void* p;
+    int dtype;
+};
+rsq_status check_aligned(const char* who, const rsq_norm_config& c, std::initializer_list<Array> arrays) {
+    for (const Array& a : arrays)
+        if (misaligned(a.p, aligned_to(c, a.dtype)))
+            return set_error(RSQ_E_INVAL, "%s: a buffer is not %u-byte aligned", who, aligned_to(c, a.dtype));
+    return RSQ_OK;
+}
 
 // Checks a configuration and fills in its defaults.
 rsq_status check_config(const char* who, const rsq_norm_config* cfg, bool residual, rsq_norm_config* out) {
@@ -643,13 +662,12 @@ rsq_status rsq_norm_workspace(const rsq_norm_config* cfg, size_t* bytes) {
 
 rsq_status rsq_gated_norm(const rsq_norm_config* cfg, const void* x, const void* z, const float* w, void* y, void* stream) {
     rsq_norm_config c;
-    const rsq_status st = check_config("gated_norm", cfg, false, &c);
+    rsq_status st = check_config("gated_norm", cfg, false, &c);
     if (st) return st;
-    if (!w || misaligned(w)) return set_error(RSQ_E_INVAL, "gated_norm: w null or not 16-byte aligned");
+    if (!w) return set_error(RSQ_E_INVAL, "gated_norm: null w");
+    if ((st = check_aligned("gated_norm", c, {{x, c.x_dtype}, {z, c.side_dtype}, {w, RSQ_F32}, {y, c.y_dtype}}))) return st;
     if (c.rows == 0) return RSQ_OK;
     if (!x || !y) return set_error(RSQ_E_INVAL, "gated_norm: null x or y");
-    for (const void* q : {x, z, static_cast<const void*>(y)})
-        if (misaligned(q)) return set_error(RSQ_E_INVAL, "gated_norm: a buffer is not 16-byte aligned");
     const Geometry g = geometry(c, false);
     NormParams p = params(c, g);
     p.x = x;
@@ -665,13 +683,14 @@ rsq_status rsq_gated_norm_backward(const rsq_norm_config* cfg, const void* x, co
                                    const void* dy, void* dx, void* dz, float* dw, void* workspace,
                                    size_t workspace_bytes, void* stream) {
     rsq_norm_config c;
-    const rsq_status st = check_config("gated_norm_backward", cfg, false, &c);
+    rsq_status st = check_config("gated_norm_backward", cfg, false, &c);
     if (st) return st;
-    if (!w || misaligned(w)) return set_error(RSQ_E_INVAL, "gated_norm_backward: w null or not 16-byte aligned");
+    if (!w) return set_error(RSQ_E_INVAL, "gated_norm_backward: null w");
     if (c.rows && (!x || !dy)) return set_error(RSQ_E_INVAL, "gated_norm_backward: null x or dy");
     if (dz && !z) return set_error(RSQ_E_INVAL, "gated_norm_backward: dz without z");
-    for (const void* q : {x, z, dy, static_cast<const void*>(dx), static_cast<const void*>(dz), static_cast<const void*>(dw)})
-        if (misaligned(q)) return set_error(RSQ_E_INVAL, "gated_norm_backward: a buffer is not 16-byte aligned");
+    if ((st = check_aligned("gated_norm_backward", c, {{x, c.x_dtype}, {z, c.side_dtype}, {w, RSQ_F32}, {dy, c.y_dtype}, {dx, c.x_dtype},
+                                                       {dz, c.side_dtype}, {dw, RSQ_F32}})))
+        return st;
     NormParams p = params(c, geometry(c, true));
     p.x = x;
     p.side = z;
@@ -686,14 +705,14 @@ rsq_status rsq_gated_norm_backward(const rsq_norm_config* cfg, const void* x, co
 rsq_status rsq_residual_norm(const rsq_norm_config* cfg, const void* x, const void* residual, const float* scale,
                              const float* w, void* h, void* y, void* stream) {
     rsq_norm_config c;
-    const rsq_status st = check_config("residual_norm", cfg, true, &c);
+    rsq_status st = check_config("residual_norm", cfg, true, &c);
     if (st) return st;
-    if (!w || misaligned(w) || misaligned(scale))
-        return set_error(RSQ_E_INVAL, "residual_norm: w null, or w or scale not 16-byte aligned");
+    if (!w) return set_error(RSQ_E_INVAL, "residual_norm: null w");
+    if ((st = check_aligned("residual_norm", c, {{x, c.x_dtype}, {residual, c.side_dtype}, {scale, RSQ_F32}, {w, RSQ_F32},
+                                                 {h, c.side_dtype}, {y, c.y_dtype}})))
+        return st;
     if (c.rows == 0) return RSQ_OK;
     if (!x || !h || !y) return set_error(RSQ_E_INVAL, "residual_norm: null x, h or y");
-    for (const void* q : {x, residual, static_cast<const void*>(h), static_cast<const void*>(y)})
-        if (misaligned(q)) return set_error(RSQ_E_INVAL, "residual_norm: a buffer is not 16-byte aligned");
     if (residual == h && c.side_stride != c.width)
         return set_error(RSQ_E_INVAL, "residual_norm: h is packed: in place needs a packed residual");
     const Geometry g = geometry(c, false);
@@ -712,16 +731,16 @@ rsq_status rsq_residual_norm_backward(const rsq_norm_config* cfg, const void* x,
                                       const float* w, const void* dy, const void* dh, void* dx, void* dresidual,
                                       float* dscale, float* dw, void* workspace, size_t workspace_bytes, void* stream) {
     rsq_norm_config c;
-    const rsq_status st = check_config("residual_norm_backward", cfg, true, &c);
+    rsq_status st = check_config("residual_norm_backward", cfg, true, &c);
     if (st) return st;
-    if (!w || misaligned(w) || misaligned(scale))
-        return set_error(RSQ_E_INVAL, "residual_norm_backward: w null, or w or scale not 16-byte aligned");
+    c.side_stride = c.width;  // h as the forward pass wrote it
+    if (!w) return set_error(RSQ_E_INVAL, "residual_norm_backward: null w");
     if (c.rows && (!h || !dy)) return set_error(RSQ_E_INVAL, "residual_norm_backward: null h or dy");
     if (c.rows && dscale && !x) return set_error(RSQ_E_INVAL, "residual_norm_backward: dscale needs x");
-    for (const void* q : {x, h, dy, dh, static_cast<const void*>(dx), static_cast<const void*>(dresidual),
-                          static_cast<const void*>(dscale), static_cast<const void*>(dw)})
-        if (misaligned(q)) return set_error(RSQ_E_INVAL, "residual_norm_backward: a buffer is not 16-byte aligned");
-    c.side_stride = c.width;  // h as the forward pass wrote it
+    if ((st = check_aligned("residual_norm_backward", c, {{x, c.x_dtype}, {h, c.side_dtype}, {scale, RSQ_F32}, {w, RSQ_F32}, {dy, c.y_dtype},
+                                                          {dh, c.side_dtype}, {dx, c.x_dtype}, {dresidual, c.side_dtype},
+                                                          {dscale, RSQ_F32}, {dw, RSQ_F32}})))
+        return st;
     NormParams p = params(c, geometry(c, true));
     p.x = x;
     p.side = h;
