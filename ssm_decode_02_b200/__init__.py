@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 import numpy as np
 
@@ -211,13 +212,15 @@ def _dptr(t) -> int | None:
 def _workspace(t) -> tuple[int | None, int]:
     if t is None:
         return None, 0
-    return _arg(t, 0, None, _device(), "workspace"), t.numel() * t.element_size()
+    return _arg(t, 0, None, _current_device(), "workspace"), t.numel() * t.element_size()
 
 
-def _current_device() -> int:
+def _current_device() -> int | None:
+    """torch's current device; None before it has one, when no argument can be a tensor on it."""
     global _current_device
-    import torch
-    torch.cuda.current_device()
+    torch = sys.modules.get("torch")
+    if torch is None or not torch.cuda.is_initialized():
+        return None
     _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     return _current_device()
 
@@ -226,20 +229,14 @@ _torch_types = None
 
 
 def _types() -> dict:
-    """torch dtypes by rsq_dtype; int32 by its name."""
+    """torch dtypes by rsq_dtype; int32 by its name.  None before torch is loaded."""
     global _torch_types
     if _torch_types is None:
-        import torch
+        torch = sys.modules.get("torch")
+        if torch is None:
+            return dict.fromkeys((RSQ_F32, RSQ_BF16, "int32"))
         _torch_types = {RSQ_F32: torch.float32, RSQ_BF16: torch.bfloat16, "int32": torch.int32}
     return _torch_types
-
-
-def _device() -> int | None:
-    """The current device; None without one, so that no tensor is on it."""
-    try:
-        return _current_device()
-    except (RuntimeError, AssertionError):
-        return None
 
 
 def _refuse(t, count: int, want, name: str) -> None:
@@ -250,7 +247,7 @@ def _refuse(t, count: int, want, name: str) -> None:
         raise ValueError("%s: expected a CUDA tensor, got one on %s" % (name, t.device))
     if t.numel() < count or (want is not None and t.dtype is not want):
         raise ValueError("%s: expected at least %d elements of %s, got %s of %s" % (name, count, want, tuple(t.shape), t.dtype))
-    raise ValueError("%s is on cuda:%d, the current device is cuda:%s" % (name, t.get_device(), _device()))
+    raise ValueError("%s is on cuda:%d, the current device is cuda:%s" % (name, t.get_device(), _current_device()))
 
 
 def _fits(t, count: int, want, here, name: str) -> None:
@@ -549,7 +546,7 @@ def rsq_scan_workspace(cfg: rsq_scan_config, backward: bool = False) -> int:
 def _scan_args(c, inputs, out, cu_seqlens, states, grads=None) -> list:
     """Checks the tensors behind a call's arguments, whose sizes, types and device the kernels
     take from the configuration; the addresses of cu_seqlens, the states and out."""
-    types, here = _types(), _device()
+    types, here = _types(), _current_device()
     f32, bf16 = types[RSQ_F32], types[RSQ_BF16]
     tokens, gates = c.tokens, c.tokens * c.heads
     x_row, b_row = c.heads * c.dv, c.ngroups * c.dk
@@ -604,7 +601,7 @@ def rsq_norm_workspace(cfg: rsq_norm_config) -> int:
 
 def rsq_gated_norm(cfg: rsq_norm_config, x, z, w, y, stream=None) -> None:
     """x and z may be row-strided, as the configuration says (norm_config reads their strides)."""
-    types, here, rows, width = _types(), _device(), cfg.rows, cfg.width
+    types, here, rows, width = _types(), _current_device(), cfg.rows, cfg.width
     args = (_arg_rows(x, rows, width, cfg.x_stride, types.get(cfg.x_dtype), here, "x"),
             _arg_rows(z, rows, width, cfg.side_stride, types.get(cfg.side_dtype), here, "z"),
             _arg(w, width, types[RSQ_F32], here, "w"), _arg(y, rows * width, types.get(cfg.y_dtype), here, "y"))
@@ -612,7 +609,7 @@ def rsq_gated_norm(cfg: rsq_norm_config, x, z, w, y, stream=None) -> None:
 
 
 def rsq_gated_norm_backward(cfg: rsq_norm_config, x, z, w, dy, dx, dz, dw, workspace=None, stream=None) -> None:
-    types, here, rows, width = _types(), _device(), cfg.rows, cfg.width
+    types, here, rows, width = _types(), _current_device(), cfg.rows, cfg.width
     n, tx, ts, f32 = rows * width, types.get(cfg.x_dtype), types.get(cfg.side_dtype), types[RSQ_F32]
     ws, ws_bytes = _workspace(workspace)
     args = (_arg_rows(x, rows, width, cfg.x_stride, tx, here, "x"), _arg_rows(z, rows, width, cfg.side_stride, ts, here, "z"),
@@ -623,7 +620,7 @@ def rsq_gated_norm_backward(cfg: rsq_norm_config, x, z, w, dy, dx, dz, dw, works
 
 def rsq_residual_norm(cfg: rsq_norm_config, x, residual, scale, w, h, y, stream=None) -> None:
     """x and residual may be row-strided, as the configuration says (norm_config reads their strides)."""
-    types, here, rows, width = _types(), _device(), cfg.rows, cfg.width
+    types, here, rows, width = _types(), _current_device(), cfg.rows, cfg.width
     n, ts, f32 = rows * width, types.get(cfg.side_dtype), types[RSQ_F32]
     args = (_arg_rows(x, rows, width, cfg.x_stride, types.get(cfg.x_dtype), here, "x"),
             _arg_rows(residual, rows, width, cfg.side_stride, ts, here, "residual"), _arg(scale, width, f32, here, "scale"),
@@ -633,7 +630,7 @@ def rsq_residual_norm(cfg: rsq_norm_config, x, residual, scale, w, h, y, stream=
 
 def rsq_residual_norm_backward(cfg: rsq_norm_config, x, h, scale, w, dy, dh, dx, dresidual, dscale, dw,
                                workspace=None, stream=None) -> None:
-    types, here, rows, width = _types(), _device(), cfg.rows, cfg.width
+    types, here, rows, width = _types(), _current_device(), cfg.rows, cfg.width
     n, tx, ts, f32 = rows * width, types.get(cfg.x_dtype), types.get(cfg.side_dtype), types[RSQ_F32]
     ws, ws_bytes = _workspace(workspace)
     args = (_arg_rows(x, rows, width, cfg.x_stride, tx, here, "x"), _arg(h, n, ts, here, "h"), _arg(scale, width, f32, here, "scale"),

@@ -309,3 +309,33 @@ def test_the_functions_check_as_the_class_does(calls):
     rsq.rsq_scan(cfg, rsq.rsq_scan_inputs(P, P, P, P, P, None, None, 0, 0, 0), P)     # addresses alone
     rsq.rsq_scan_backward(cfg, ins, out, rsq.rsq_scan_grads(dx=P), state_in=state)
     assert calls.names == ["rsq_scan", "rsq_scan", "rsq_scan_backward"]
+
+
+def test_addresses_need_no_torch():
+    """A program that has addresses alone, and a stream, loads no torch and starts none of its CUDA."""
+    import subprocess
+    import sys
+    code = """
+import ctypes, sys
+import ssm_decode_02_b200 as rsq
+assert "torch" not in sys.modules
+rsq.lib = type("Calls", (), {"__getattr__": lambda s, n: (lambda *a: rsq.RSQ_OK)})()
+P = 1 << 20
+cfg = rsq.rsq_norm_config(4, 64, 0, 0, 1, 1, 1, 1e-5, 0, 0)
+def all_calls():
+    rsq.rsq_gated_norm(cfg, P, P, P, P, stream=0)
+    rsq.rsq_gated_norm_backward(cfg, P, P, P, P, P, P, None, stream=0)
+    rsq.rsq_residual_norm(cfg, P, P, P, P, P, P, stream=0)
+    rsq.rsq_residual_norm_backward(cfg, P, P, P, P, P, P, P, P, None, None, stream=0)
+    scan = rsq.rsq_scan_config(rsq.RSQ_MAMBA2, rsq.RSQ_BF16, 1, 1, 64, 64, 1, 0, 4)
+    ins = rsq.scan_inputs(P, P, P, P, P)
+    rsq.rsq_scan(scan, ins, P, state_in=P, state_out=P, stream=0)
+    rsq.rsq_scan_backward(scan, ins, P, rsq.scan_grads(dx=P), state_in=P, stream=0)
+all_calls()
+assert "torch" not in sys.modules
+import torch
+all_calls()
+assert not torch.cuda.is_initialized()
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=rsq.os.path.dirname(rsq.os.path.dirname(rsq.__file__)))
+    assert r.returncode == 0, r.stderr[-2000:]
