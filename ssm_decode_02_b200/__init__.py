@@ -289,18 +289,18 @@ def _arg_rows(t, rows: int, width: int, stride: int, want, here, name: str) -> i
     _fits(t, rows * width, want, here, name)
     if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError("%s: expected a contiguous last dimension" % name)
-    if rows > 1:
-        stride, inner = stride or width, 1
-        for d in range(t.dim() - 1, 0, -1):     # the columns of a row, as far as they are packed
-            if t.shape[d] > 1 and t.stride(d) != inner:
-                break
-            inner *= t.shape[d]
-        else:
-            if t.dim() > 1 and t.stride(0) == stride and t.shape[0] >= rows and inner >= width:
-                return t.data_ptr()
-        raise ValueError("%s: the configuration has %d rows of %d columns, %d elements apart; got shape %s with strides %s"
-                         % (name, rows, width, stride, tuple(t.shape), tuple(t.stride())))
-    return t.data_ptr()
+    if rows < 2 and t.is_contiguous():
+        return t.data_ptr()
+    stride, inner = stride or width, 1
+    for d in range(t.dim() - 1, 0, -1):     # the columns of a row, as far as they are packed
+        if t.shape[d] > 1 and t.stride(d) != inner:
+            break
+        inner *= t.shape[d]
+    else:
+        if t.dim() > 1 and inner >= width and (rows < 2 or (t.stride(0) == stride and t.shape[0] >= rows)):
+            return t.data_ptr()
+    raise ValueError("%s: the configuration has %d rows of %d columns, %d elements apart; got shape %s with strides %s"
+                     % (name, rows, width, stride, tuple(t.shape), tuple(t.stride())))
 
 
 def _dtype_of(t) -> int:

@@ -131,7 +131,8 @@ def test_norms_refuse_rows_that_lie_other_than_configured(calls):
              (norm_cfg(x_stride=apart), on(T - 1, apart, dtype=BF)[:, :N], packed),
              (norm_cfg(x_stride=apart), on(T, apart, dtype=BF)[:, :N - 8], None),
              (norm_cfg(), on(1, N, dtype=BF).expand(T, N), packed), (norm_cfg(), packed, on(1, N, dtype=BF).expand(T, N)),
-             (norm_cfg(x_stride=apart), on(T, 2, apart // 2, dtype=BF)[:, :, :N // 2], None)]
+             (norm_cfg(x_stride=apart), on(T, 2, apart // 2, dtype=BF)[:, :, :N // 2], None),
+             (norm_cfg(rows=1), on(1, 2, apart // 2, dtype=BF)[:, :, :N // 2], None)]
     for cfg, x, side in wrong:
         for call in norm_calls(cfg, x, side):
             with pytest.raises(ValueError):
@@ -147,7 +148,8 @@ def test_norms_take_rows_as_configured(calls):
     apart = int(a.stride(0))
     right = [(norm_cfg(), packed, packed), (norm_cfg(x_stride=N, side_stride=N), packed, packed), (norm_cfg(x_stride=apart), a, packed),
              (norm_cfg(x_stride=apart, side_stride=apart), a, b), (norm_cfg(), packed.view(T * N), packed.view(T // 2, 2 * N)),
-             (norm_cfg(rows=1), a[:1], b[:1]), (norm_cfg(x_stride=apart), a.view(T, 2, N // 2), None), (norm_cfg(rows=T - 3), packed, packed)]
+             (norm_cfg(rows=1), a[:1], b[:1]), (norm_cfg(x_stride=apart), a.view(T, 2, N // 2), None), (norm_cfg(rows=T - 3), packed, packed),
+             (norm_cfg(rows=1, x_stride=apart), packed.view(T * N), packed), (norm_cfg(rows=0, x_stride=apart), a[:0], None)]
     for cfg, x, side in right:
         for call in norm_calls(cfg, x, side):
             call()
