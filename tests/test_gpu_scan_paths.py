@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import ssm_decode_02_b200 as rsq
-from test_gpu_scan import check_backward, check_forward, cuda, inputs, make, poison, reference_grads, shape
+from scan_reference import scan64
+from test_gpu_scan import check_backward, check_forward, cuda, dbl, inputs, make, poison, reference_grads, shape
 
 pytestmark = pytest.mark.gpu
 
@@ -40,8 +41,10 @@ def run(d, bounds, *, ragged, apart=False, in_place=False, dout=None, dstate=Non
     full = lambda t: torch.full(t.shape, 7.0, dtype=t.dtype, device="cuda")  # noqa: E731
     g = {"dx": full(d["x"]), "dBm": full(d["Bm"]), "dCm": full(d["Cm"]), "dlog_decay": torch.full((T, H), 7.0, device="cuda"),
          "dstate_in": dstate.cuda() if in_place else torch.empty((n, H, N, P), device="cuda")}
+    if d["dt"] is not None:
+        g["ddt"] = full(d["dt"])
     if d["decay"] is None:
-        g |= {"ddt": full(d["dt"]), "dA": full(d["A"])}
+        g["dA"] = full(d["A"])
     if d["D"] is not None:
         g["dD"] = full(d["D"])
     doutc = dout.cuda()
@@ -122,6 +125,64 @@ def test_strong_decays_and_restarts_on_tensor_cores(H, N, P, G, decay):
     check_all(d, bounds, got, dout, dstate)
     if decay:
         assert (d["decay"] == 0).any() and (got[2]["dlog_decay"][d["decay"] == 0] == 0).all()
+
+
+# ------------------------------------------------------------------------------- inputs and requests
+@pytest.mark.parametrize("n,tokens,H,N,P", [(3, 9, 2, 64, 64), (1, 270, 3, 32, 32), (2, 600, 2, 64, 64), (2, 300, 2, 256, 128)])
+def test_dt_beside_a_given_decay(n, tokens, H, N, P):
+    """dt weights the tokens and the decay is given: ddt has no way through exp(dt A)."""
+    d, bounds = make(n, tokens, H, N, P, 1, decay=True, seed=91)
+    d["dt"] = torch.nn.functional.softplus(torch.randn(tokens, H, generator=torch.Generator().manual_seed(92)) - 1)
+    dout, dstate = gradients_of(d, n, 93)
+    out, state, got = run(d, bounds, ragged=False, dout=dout, dstate=dstate)
+    check_forward(d, bounds, out, state)
+    want = reference_grads(d, bounds, dout, dstate)
+    v = dbl(d)
+    v["dt"].requires_grad_()
+    o, f = scan64(**v, bounds=bounds)
+    want["ddt"], = torch.autograd.grad((o * dout.double()).sum() + (f * dstate.double()).sum(), [v["dt"]])
+    check_backward(d, bounds, got, want)
+
+
+@pytest.mark.parametrize("H,N,P", [(3, 32, 32), (2, 64, 64), (2, 256, 64)])
+def test_each_gradient_by_itself(H, N, P):
+    """What is asked for does not depend on what else is."""
+    d, bounds = make(2, 2 * 150, H, N, P, 1, seed=95)
+    dout, dstate = gradients_of(d, 2, 96)
+    all_of = run(d, bounds, ragged=False, dout=dout, dstate=dstate)[2]
+    c, s = cuda(d), shape(d, 2)
+    for name, want in all_of.items():
+        t = torch.full(want.shape, 7.0, dtype=want.dtype, device="cuda")
+        s.backward(inputs(c), dout.cuda(), rsq.scan_grads(**{name: t}), state_in=c["state_in"], dstate_out=dstate.cuda(),
+                   workspace=poison(s.alloc_workspace(backward=True)))
+        assert torch.equal(t.cpu(), want), name
+
+
+def test_segments_of_a_ragged_batch_in_a_graph():
+    """Captured once, replayed on other inputs and other bounds."""
+    n, H, N, P = len(SEGMENTED) - 1, 2, 64, 64
+    d, bounds = make(n, ROWS, H, N, P, 1, bounds=SEGMENTED, seed=97)
+    e, other = make(n, ROWS, H, N, P, 1, bounds=[0, 12, 4700, 4700, 4701, 9700], seed=98)
+    c, s = cuda(d), rsq.Scan(n, ROWS, H, N, P, ragged=True)
+    cu = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    out, state, ws = torch.full_like(c["x"], 7.0), c["state_in"].clone(), poison(s.alloc_workspace())
+
+    def call():
+        s.forward(inputs(c), out, state_in=state, state_out=state, cu_seqlens=cu, workspace=ws)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for k, v in cuda(e).items():
+        if v is not None:
+            c[k].copy_(v)
+    cu.copy_(torch.tensor(other, dtype=torch.int32))
+    state.copy_(c["state_in"])
+    out.fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    rsq.rsq_scan_check(ws)
+    check_forward(e, other, out.cpu(), state.cpu())
 
 
 # ------------------------------------------------------------------------------------------ failure mark
