@@ -469,10 +469,11 @@ rsq_status rsq_pipe_streams(const rsq_pipe* pipe, void** copy_in, void** compute
  *              after the other.  1: sequence i has the rows cu_seqlens[i] ..
  *              cu_seqlens[i+1] - 1; cu_seqlens is a device int32 array
  *              [sequences + 1], not decreasing, within [0, tokens] (a bound
- *              outside is clamped into the array and to the bound before it;
- *              nothing outside is read or written).  A sequence may be empty:
- *              its state_out is its state_in.  Rows of no sequence are neither
- *              read nor written.
+ *              outside is clamped into the array, and the end of a sequence to its
+ *              beginning: nothing outside of the array is read or written; rows that
+ *              several sequences then share, and their states, are undefined).  A
+ *              sequence may be empty: its state_out is its state_in.  Rows of no
+ *              sequence are neither read nor written.
  *
  * rsq_scan_inputs (device)
  *   x   [tokens][heads][dv], Bm, Cm [tokens][ngroups][dk] in in_dtype; consecutive

@@ -3,20 +3,23 @@
 //
 // A unit is one group of columns of one row.  Its threads keep the unit in
 // registers between the reduction and the output, so that every input is read
-// once and every output written once: the kernels are bound by HBM.  A block
-// walks down the rows with its columns fixed (grid.y = group), loads the next
-// row's vectors before it reduces the current one, and in the backward pass
-// adds up the column sums (dw, dscale) of its rows in shared memory; a second
-// kernel adds the blocks' partial sums in block order.
+// once and every output written once: the forward kernels are bound by HBM.  A
+// block walks down the rows with its columns fixed (grid.y = group), a row at a time:
+// load, reduce, write; the other blocks of the SM load meanwhile.  In the backward
+// pass it adds up the column sums (dw, dscale) of its rows in shared memory; a
+// second kernel adds the blocks' partial sums in block order.
 //
 // With n = u r, r = 1/sqrt(mean(u^2) + eps) and dn the gradient of n:
 //     du = r (dn - n mean(dn n)),   mean(dn n) = r mean(dn u)
 // so the two sums of a backward row, u^2 and dn u, share one reduction.
 //
-// Measured: gated norm of 16384 x 5120 bf16 84 us (6.0 TB/s, 91% of the measured copy
-// rate), residual norm of as many bytes 88 us; gradients 96 us (8192 x 5120, 420 MB) and
-// 80 us (8192 x 2560 with a binary32 stream, 378 MB), 66 and 72% -- bound by the chain of a
-// row (load, two passes, reduction), of which 96 registers a thread let an SM hold few.
+// Measured: gated norm of 16384 x 5120 bf16 84 to 91 us (5.5 to 6.0 TB/s, 84 to 91% of the
+// measured copy rate), residual norm of as many bytes 89 us; gradients 96 us (8192 x 5120,
+// 420 MB) and 79 us (8192 x 2560 with a binary32 stream, 378 MB), 67 and 73%, with 20 of
+// an SM's 64 warps at 96 registers a thread.  The gated one issues in 64% of its slots, and
+// its warps wait for global loads (2.2 of 7.7 cycles an instruction), their turn (1.5) and
+// shared memory and the special functions (0.9); the residual one issues in 40%, with 4.1 of
+// 12.2 cycles on global loads and 3.6 on the sums and weights in shared memory.
 // Rows on their way to shared memory by cp.async (107 to 159 us), paired binary32
 // arithmetic (135), one vector a thread (126 to 170) and fewer registers (spills) were
 // slower.  A step's few rows are one launch: 3 us in a graph.
@@ -309,10 +312,9 @@ template <int VEC, int K>
 constexpr bool kKeepCols = VEC * K <= 16;
 
 // Backward.  Between the loads of a row and its stores lie two passes over its
-// elements and one reduction.  What bounds it is how many rows an SM can have in
-// that chain, so registers hold the row as loaded and its sigmoids alone, and the
-// second pass makes u and dn again; w, scale and the column sums lie in shared
-// memory at places of the thread's own.
+// elements and one reduction.  For room for more rows in that chain, registers hold
+// the row as loaded and its sigmoids alone, and the second pass makes u and dn again;
+// w, scale and the column sums lie in shared memory at places of the thread's own.
 template <int MODE, class TX, class TS, class TY, int VEC, int K>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__(VEC * K <= 16 && VEC == 8 ? kBackwardRegs : 128)
 norm_backward_kernel(const __grid_constant__ NormParams p) {

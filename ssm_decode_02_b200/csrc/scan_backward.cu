@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) dx_kernel(const __grid_constant__
                 const int t = lane * 4 + k;
                 if (t >= valid) continue;
                 const long long at = static_cast<long long>(rg.first + t) * p.H + h;
-                if (p.decay && __ldg(p.decay + at) == 0.f) dl[k] = 0.f;  // nothing passes: the sums only cancel to rounding
+                if (p.decay && __ldg(p.decay + at) == 0.f) dl[k] = 0.f;  // nothing passes, not 0 times a non-finite value either
                 if (p.dlog) p.dlog[at] = dl[k];
                 if (p.ddt) p.ddt[at] = p.decay ? dir[k] : fmaf(ah, dl[k], dir[k]);
                 da = fmaf(dt4[k], dl[k], da);

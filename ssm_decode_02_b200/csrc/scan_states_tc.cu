@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kBlock, 1) states_tc_kernel(const __grid_const
                     if constexpr (F32)
                         (ps.rev ? p.df : p.sf)[cell + k * kTile] = S[k];
                     else
-                        p.sh[cell + k * kTile] = __float2bfloat16_rn(S[k]);
+                        p.sh[cell + k * kTile] = __float2bfloat16_rn(S[k]);   // an operand for out alone (scan.cuh, Roundings)
                 }
             }
             const float a = ex2(end.x + end.y);
