@@ -481,7 +481,7 @@ rsq_status rsq_pipe_streams(const rsq_pipe* pipe, void** copy_in, void** compute
  *       least the row and a multiple of 8), so that they may be slices of one
  *       projection's output.  16-byte alignment, as the outputs and states.
  *   dt  float [tokens][heads] or NULL (1).  A, D  float [heads]; D NULL: 0.
- *   decay float [tokens][heads], values >= 0 (0 restarts the state), or NULL:
+ *   decay float [tokens][heads], values >= 0 (0 restarts a finite state), or NULL:
  *       exp(dt A), which needs dt and A (arrays of no tokens may be NULL).
  *   These arrays, their gradients and cu_seqlens need only 4-byte alignment, so
  *   that a call may take a piece of a longer array.

@@ -185,6 +185,18 @@ def test_segments_of_a_ragged_batch_in_a_graph():
     check_forward(e, other, out.cpu(), state.cpu())
 
 
+@pytest.mark.parametrize("N,P", [(32, 32), (64, 64), (256, 64)])
+def test_no_gradient_of_a_restart_beside_a_nan(N, P):
+    """A decay of zero has no gradient, whatever stands on the other side of it.  A token's x is in the
+    gradients of the decays behind it, so those of 41 to 49 are no numbers."""
+    d, bounds = make(1, 300, 2, N, P, 1, decay=True, seed=99)
+    d["decay"][50] = 0.0
+    d["x"][40] = float("nan")
+    dout, dstate = gradients_of(d, 1, 100)
+    dlog = run(d, bounds, ragged=False, dout=dout, dstate=dstate)[2]["dlog_decay"]
+    assert (dlog[50] == 0).all() and torch.isnan(dlog[41:50]).any()
+
+
 # ------------------------------------------------------------------------------------------ failure mark
 @pytest.mark.parametrize("tokens", [0, 2, 24])
 def test_a_call_of_single_tokens_clears_the_mark_of_a_workspace_that_it_is_given(tokens):
