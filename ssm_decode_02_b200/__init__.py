@@ -284,14 +284,21 @@ def _arg_rows(t, rows: int, width: int, stride: int, want, here, name: str) -> i
     the configuration, whichever tensors it was made from."""
     if t is None or isinstance(t, int):
         return t
-    if (stride == width or not stride) and hasattr(t, "is_contiguous") and t.is_contiguous():
-        return _arg(t, rows * width, want, here, name)
+    stride = stride or width
+    try:
+        if stride == width and t.is_contiguous():
+            return _arg(t, rows * width, want, here, name)
+        if (t.dim() == 2 and t.stride(0) == stride and t.stride(1) == 1 and t.shape[0] >= rows and t.shape[1] >= width
+                and (t.dtype is want or want is None) and t.get_device() == here):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _fits(t, rows * width, want, here, name)
     if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError("%s: expected a contiguous last dimension" % name)
     if rows < 2 and t.is_contiguous():
         return t.data_ptr()
-    stride, inner = stride or width, 1
+    inner = 1
     for d in range(t.dim() - 1, 0, -1):     # the columns of a row, as far as they are packed
         if t.shape[d] > 1 and t.stride(d) != inner:
             break
@@ -706,10 +713,11 @@ def scan_inputs(x, Bm, Cm, dt=None, A=None, D=None, decay=None) -> rsq_scan_inpu
     result keeps the tensors that it points at."""
     (xp, xs), (bp, bs), (cp, cs) = _token_rows(x, "x"), _token_rows(Bm, "Bm"), _token_rows(Cm, "Cm")
     types = _types()
-    for name, t, type_ in (("x", x, RSQ_BF16), ("Bm", Bm, RSQ_BF16), ("Cm", Cm, RSQ_BF16), ("dt", dt, RSQ_F32), ("A", A, RSQ_F32),
-                           ("D", D, RSQ_F32), ("decay", decay, RSQ_F32)):
-        if t is not None and not isinstance(t, int) and t.dtype is not types[type_]:
-            raise ValueError("%s: expected %s, got %s" % (name, types[type_], t.dtype))
+    bf16, f32 = types[RSQ_BF16], types[RSQ_F32]
+    for name, t, want in (("x", x, bf16), ("Bm", Bm, bf16), ("Cm", Cm, bf16), ("dt", dt, f32), ("A", A, f32), ("D", D, f32),
+                          ("decay", decay, f32)):
+        if t is not None and not isinstance(t, int) and t.dtype is not want:
+            raise ValueError("%s: expected %s, got %s" % (name, want, t.dtype))
     ins = rsq_scan_inputs(xp, bp, cp, _dptr(dt), _dptr(A), _dptr(D), _dptr(decay), xs, bs, cs)
     ins.tensors = (x, Bm, Cm, dt, A, D, decay)
     return ins
