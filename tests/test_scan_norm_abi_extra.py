@@ -40,3 +40,21 @@ def test_misaligned_arrays_are_refused(width, dtype, off):
     each(lambda a: lib.rsq_gated_norm_backward(cfg, *a, None, 0, 0), 7, skip=())      # and a dw needs a workspace
     each(lambda a: lib.rsq_residual_norm(cfg, *a, 0), 6, skip=())
     each(lambda a: lib.rsq_residual_norm_backward(cfg, *a, None, 0, 0), 10)
+
+
+def bytes_without_segments(slots, H, N, P, backward):
+    """The workspace of a scan whose sequences are not cut into segments."""
+    cells, state = slots * H, N * 64 * -(-P // 64)
+    sizes = [4, slots * 8, cells * 128 * 8, cells * 128 * 4]
+    sizes += [cells * state * 4, cells * state * 4, 2 * cells * 4] if backward else [cells * state * 2]
+    return sum(-(-k // 256) * 256 for k in sizes)
+
+
+@pytest.mark.parametrize("tokens,H,N,P,segments", [(128 * 40 + 17, 2, 16, 16, True), (128 * 33 + 5, 1, 16, 16, True),
+                                                   (128 * 18 + 70, 2, 64, 64, True), (128 * 15, 2, 64, 64, False), (128 * 40, 80, 128, 64, False)])
+def test_which_sequences_are_cut_into_segments(tokens, H, N, P, segments):
+    """The long sequences of the GPU tests are, forward and backward: a change of the rule shows here."""
+    s = rsq.Scan(1, tokens, H, N, P)
+    for got, backward in ((s.workspace_bytes, False), (s.backward_workspace_bytes, True)):
+        whole = bytes_without_segments(-(-tokens // 128), H, N, P, backward)
+        assert (got > whole) if segments else (got == whole), backward
